@@ -1,0 +1,79 @@
+// lf_paged.cuh -- host/device interface of the rotation, the paged cache
+// append and the paged decode (include/lf_paged.h).
+#pragma once
+
+#include "lf_common.cuh"
+#include "lf_paged.h"
+#include "lf_pages.cuh"
+
+#define LF_ROPE_MAX_PAIRS 32
+#define LF_ROPE_MAX_AXES 4
+#define LF_ROPE_MAX_JOBS 8
+
+// details of LF_ERR_DEVICE_INPUT in the status word (+ the sequence)
+#define LF_DET_LENGTH 4000000   // length outside [0, capacity]
+#define LF_DET_PAGE 5000000     // block table entry outside [0, num_pages)
+#define LF_DET_PREFIX 6000000   // prefix table entry outside [0, num_pages)
+#define LF_DET_TOKENS 7000000   // new tokens without a row, or cu_new not ascending
+
+// Turns (angle / 2 pi) per position of each pair, as hi + lo.
+struct LfRopeDev {
+  int pairs, interleaved, n_axes;
+  float sign;  // +1 forward, -1 backward
+  double hi[LF_ROPE_MAX_PAIRS], lo[LF_ROPE_MAX_PAIRS];
+  uint8_t axis[LF_ROPE_MAX_PAIRS];
+};
+
+// One tensor of a rotation or append: out == nullptr with pool != nullptr
+// writes head h of a token to its row of that pool.
+struct LfRopeJob {
+  const void *x;
+  void *out;
+  void *pool;
+  int heads;
+  int rotate;
+  int64_t xs[3], os[3];  // batch, head, token
+};
+
+struct LfRopeArgs {
+  LfRopeDev r;
+  LfRopeJob job[LF_ROPE_MAX_JOBS];
+  int heads_total;
+  int heads_per_block;  // heads a thread works through
+  int n;                // tokens per sequence (rotation)
+  int64_t tokens;       // tokens in all
+  const int32_t *positions;
+  // append
+  int B, Hkv, shift, num_pages, max_pages, pos_offset;
+  const int32_t *cu, *lengths, *table;
+  int32_t *status;
+};
+
+// Split of the shared prefix: its keys in `nch` chunks of `chunk`.
+struct LfPagedDev {
+  int B, H, Hkv, G;      // G = H / Hkv
+  int shift, num_pages, max_pages;
+  int window, prefix_len, nch, chunk;
+  float scale_log2;
+  int64_t qs[2];         // q strides: sequence, head
+  const int32_t *table, *lengths, *prefix_table;
+  int32_t *status;
+  float *part_acc;       // [Hkv * B * G][nch][64]
+  float2 *part_ml;       // [Hkv * B * G][nch]
+  int dil[LF_MAX_H];     // per key/value head
+};
+
+cudaError_t lf_launch_rope(const LfRopeArgs &a, int dtype, bool append, cudaStream_t stream);
+
+struct LfPagedLaunch {
+  LfPagedDev dev;
+  size_t off_acc, off_ml, total;  // workspace
+  int dtype;
+  cudaStream_t stream;
+};
+
+cudaError_t lf_launch_paged_decode(const LfPagedLaunch &L, const void *q, const void *kp,
+                                   const void *vp, void *o, float *lse);
+cudaError_t lf_launch_prefix(const LfPagedLaunch &L, const void *q, const void *kp, const void *vp);
+// chunks and keys per chunk of the prefix split
+void lf_prefix_plan(LfPagedDev &d, int dtype);

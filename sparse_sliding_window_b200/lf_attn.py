@@ -1,4 +1,5 @@
-"""Thin ctypes binding of liblf_attn.so (include/lf_attn.h).
+"""Thin ctypes binding of liblf_attn.so (include/lf_attn.h, lf_proj.h,
+lf_paged.h).
 
 Argument marshalling only: torch tensors supply device memory and the CUDA
 stream; every step of the attention runs in the library's kernels.  The
@@ -28,6 +29,8 @@ EXPORTS = ["lf_attn_version", "lf_attn_workspace_size", "lf_attn_fwd", "lf_attn_
            "lf_attn_set_test_hooks", "lf_attn_cross_workspace_size", "lf_attn_cross_fwd"]
 # every symbol include/lf_proj.h declares
 PROJ_EXPORTS = ["lf_proj_workspace_size", "lf_proj_in", "lf_proj_out", "lf_proj_set_timing_events"]
+# every symbol include/lf_paged.h declares
+PAGED_EXPORTS = ["lf_rope_fwd", "lf_rope_bwd", "lf_paged_workspace_size", "lf_cache_append", "lf_paged_decode"]
 LF_STATIC_WORKSPACE_BYTES = 16 << 20
 
 
@@ -53,6 +56,24 @@ class lf_cross_params(ctypes.Structure):
 class lf_proj_params(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("n", ctypes.c_int), ("H", ctypes.c_int),
                 ("head_dim", ctypes.c_int), ("dtype", ctypes.c_int)]
+
+
+class lf_rope_params(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int), ("interleaved", ctypes.c_int), ("n_axes", ctypes.c_int),
+                ("pair_axis", ctypes.POINTER(ctypes.c_int32)), ("freqs", ctypes.POINTER(ctypes.c_double)),
+                ("base", ctypes.c_double)]
+
+
+class lf_rope_tensor(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("heads", ctypes.c_int),
+                ("x_stride", ctypes.c_int64 * 3), ("out_stride", ctypes.c_int64 * 3)]
+
+
+class lf_paged_params(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("Hkv", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("num_pages", ctypes.c_int), ("max_pages", ctypes.c_int),
+                ("window", ctypes.c_int), ("dilation", ctypes.POINTER(ctypes.c_int32)), ("scale", ctypes.c_float),
+                ("dtype", ctypes.c_int), ("prefix_len", ctypes.c_int)]
 
 
 _lib = None
@@ -101,6 +122,16 @@ def load(path: str = LIB_PATH):
         lib.lf_proj_out.restype = i32
         lib.lf_proj_set_timing_events.argtypes = [vp, vp]
         lib.lf_proj_set_timing_events.restype = i32
+        RP, GP = ctypes.POINTER(lf_rope_params), ctypes.POINTER(lf_paged_params)
+        for f in (lib.lf_rope_fwd, lib.lf_rope_bwd):
+            f.argtypes = [RP, i32, i32, i32, i32, ctypes.POINTER(lf_rope_tensor), vp, vp]
+            f.restype = i32
+        lib.lf_paged_workspace_size.argtypes = [GP]
+        lib.lf_paged_workspace_size.restype = sz
+        lib.lf_cache_append.argtypes = [GP, RP, i32] + [vp] * 3 + [ctypes.POINTER(ctypes.c_int64)] + [vp] * 8 + [sz, vp]
+        lib.lf_cache_append.restype = i32
+        lib.lf_paged_decode.argtypes = [GP, vp, ctypes.POINTER(ctypes.c_int64)] + [vp] * 8 + [sz, vp]
+        lib.lf_paged_decode.restype = i32
         _lib = lib
     return _lib
 
@@ -284,6 +315,203 @@ def lf_proj_set_timing_events(ev_start, ev_stop):
     a = None if ev_start is None else ev_start.cuda_event
     b = None if ev_stop is None else ev_stop.cuda_event
     _check(load().lf_proj_set_timing_events(a, b))
+
+
+# ------------------------------------- rotation, paged cache, paged decode --
+#
+# These calls check shapes, dtypes and devices here: the library sees bare
+# pointers, and a wrong shape would send a kernel out of its buffers.
+
+def _bad(msg: str):
+    raise LfError(LF_ERR_INVALID, msg)
+
+
+def _want(name: str, t, shape, dtype, dev, packed: bool = True):
+    """t is a CUDA tensor of this shape, dtype and device; packed: contiguous,
+    else only its last dimension."""
+    if t.shape != shape:
+        _bad("%s has shape %s, %s is wanted" % (name, tuple(t.shape), tuple(shape)))
+    if t.dtype is not dtype:
+        _bad("%s is %s, %s is wanted" % (name, t.dtype, dtype))
+    if t.device != dev:
+        _bad("%s is on %s, the call on %s" % (name, t.device, dev))
+    if not t.is_contiguous() and (packed or t.stride(-1) != 1):
+        _bad("%s is not contiguous%s" % (name, "" if packed else " in its last dimension"))
+
+
+def _cuda_device(t, name: str):
+    if not t.is_cuda:
+        _bad("%s is not on a GPU" % name)
+    return t.device
+
+
+def _launch(dev, stream, fn, *args):
+    """fn(*args, stream) with dev as the current device; stream None: dev's current stream."""
+    import torch
+    if stream is not None and stream.device != dev:
+        _bad("the stream is on %s, the tensors on %s" % (stream.device, dev))
+    if torch.cuda.current_device() == dev.index:
+        _check(fn(*args, (stream or torch.cuda.current_stream(dev)).cuda_stream))
+        return
+    with torch.cuda.device(dev):
+        _check(fn(*args, (stream or torch.cuda.current_stream(dev)).cuda_stream))
+
+
+def _torch_dtype(code: int):
+    import torch
+    return (torch.float32, torch.bfloat16, torch.float16)[code]
+
+
+def _dtype_of(t, name: str) -> int:
+    import torch
+    code = {torch.float32: LF_F32, torch.bfloat16: LF_BF16, torch.float16: LF_F16}.get(t.dtype)
+    if code is None:
+        _bad("%s is %s: float32, bfloat16 or float16 is wanted" % (name, t.dtype))
+    return code
+
+
+def make_rope_params(rot_dim: int = 64, interleaved: bool = False, n_axes: int = 1,
+                     pair_axis: Optional[Sequence[int]] = None, freqs: Optional[Sequence[float]] = None,
+                     base: float = 10000.0):
+    """Build an lf_rope_params (the arrays are kept alive on it)."""
+    r = lf_rope_params()
+    r.rot_dim, r.interleaved, r.n_axes, r.base = rot_dim, int(interleaved), n_axes, float(base)
+    for field, values, kind in (("pair_axis", pair_axis, ctypes.c_int32), ("freqs", freqs, ctypes.c_double)):
+        if values is not None:
+            if len(values) != (rot_dim or 64) // 2:
+                _bad("%s has %d entries for %d pairs" % (field, len(values), (rot_dim or 64) // 2))
+            arr = (kind * len(values))(*values)
+            setattr(r, "_%s_keep" % field, arr)
+            setattr(r, field, ctypes.cast(arr, ctypes.POINTER(kind)))
+    return r
+
+
+def _rope(fn, r, xs, outs, positions, stream):
+    if not 1 <= len(xs) <= 8 or len(outs) != len(xs):
+        _bad("1 to 8 tensors are wanted, and an output for each")
+    first = xs[0]
+    dev, code = _cuda_device(first, "x"), _dtype_of(first, "x")
+    if first.dim() != 4:
+        _bad("x has %d dimensions, [B, heads, n, 64] is wanted" % first.dim())
+    B, _, n, _ = first.shape
+    arr = (lf_rope_tensor * len(xs))()
+    for t, x, out in zip(arr, xs, outs):
+        if x.dim() != 4:
+            _bad("x has %d dimensions, [B, heads, n, 64] is wanted" % x.dim())
+        shape = (B, x.shape[1], n, 64)
+        _want("x", x, shape, first.dtype, dev, False)
+        _want("out", out, shape, first.dtype, dev, False)
+        t.x, t.out, t.heads = x.data_ptr(), out.data_ptr(), shape[1]
+        t.x_stride[:], t.out_stride[:] = x.stride()[:3], out.stride()[:3]
+    if positions is not None:
+        import torch
+        _want("positions", positions, (r.n_axes, B, n), torch.int32, dev)
+    _launch(dev, stream, fn, ctypes.byref(r), B, n, code, len(xs), arr, _ptr(positions))
+
+
+def lf_rope_fwd(r, xs, outs, positions=None, stream=None):
+    """Rotate every x [B, heads, n, 64] of xs into its out (which may be x)
+    by positions int32 [n_axes, B, n] (None: the token index)."""
+    _rope(load().lf_rope_fwd, r, xs, outs, positions, stream)
+
+
+def lf_rope_bwd(r, grads, outs, positions=None, stream=None):
+    """The backward of lf_rope_fwd: gradients of its outputs -> of its inputs."""
+    _rope(load().lf_rope_bwd, r, grads, outs, positions, stream)
+
+
+def make_paged_params(B: int, H: int, Hkv: int, page_size: int, num_pages: int, max_pages: int, window: int = -1,
+                      dilation: Optional[Sequence[int]] = None, scale: float = 0.0, dtype: int = LF_BF16,
+                      prefix_len: int = 0, head_dim: int = 64):
+    """Build an lf_paged_params (the dilation array is kept alive on it)."""
+    p = lf_paged_params()
+    p.B, p.H, p.Hkv, p.head_dim, p.page_size = B, H, Hkv, head_dim, page_size
+    p.num_pages, p.max_pages, p.window, p.scale, p.dtype, p.prefix_len = (num_pages, max_pages, window, float(scale),
+                                                                          dtype, prefix_len)
+    if dilation is not None:
+        if len(dilation) != Hkv:
+            _bad("dilation has %d entries for %d key/value heads" % (len(dilation), Hkv))
+        arr = (ctypes.c_int32 * Hkv)(*[int(x) for x in dilation])
+        p._dil_keep = arr  # type: ignore[attr-defined]
+        p.dilation = ctypes.cast(arr, ctypes.POINTER(ctypes.c_int32))
+    return p
+
+
+def lf_paged_workspace_size(p) -> int:
+    return int(load().lf_paged_workspace_size(ctypes.byref(p)))
+
+
+def paged_workspace(p, device="cuda"):
+    """Allocate a workspace for lf_cache_append and lf_paged_decode."""
+    import torch
+    nbytes = lf_paged_workspace_size(p)
+    if nbytes == 0:
+        _check(LF_ERR_INVALID)
+    return torch.zeros(nbytes, dtype=torch.uint8, device=device)  # status words start at zero
+
+
+def _paged(p, k_pages, v_pages, block_table, lengths, ws):
+    """The checks that append and decode share; returns (torch dtype, device)."""
+    import torch
+    dev = _cuda_device(k_pages, "k_pages")
+    if p.dtype not in (LF_F32, LF_BF16, LF_F16):
+        _bad("bad dtype %d" % p.dtype)
+    dt = _torch_dtype(p.dtype)
+    pool = (p.num_pages, p.Hkv, p.page_size, p.head_dim)
+    _want("k_pages", k_pages, pool, dt, dev)
+    _want("v_pages", v_pages, pool, dt, dev)
+    _want("block_table", block_table, (p.B, p.max_pages), torch.int32, dev)
+    _want("lengths", lengths, (p.B,), torch.int32, dev)
+    if ws.dtype is not torch.uint8 or ws.device != dev or not ws.is_contiguous():
+        _bad("the workspace is a contiguous uint8 tensor on %s" % dev)
+    return dt, dev
+
+
+def lf_cache_append(p, rope, q, k, v, lengths, block_table, q_out, k_pages, v_pages, ws, cu_new=None,
+                    positions=None, stream=None):
+    """Append new tokens to the paged cache: q [T,H,64] (or None), k, v
+    [T,Hkv,64], any strides (a projection's [1,H,T,64] is x[0].transpose(0, 1));
+    K rotated by rope (None: not) and V go to the pages, rotated Q to q_out."""
+    import torch
+    dt, dev = _paged(p, k_pages, v_pages, block_table, lengths, ws)
+    T = k.shape[0]
+    _want("k", k, (T, p.Hkv, 64), dt, dev, False)
+    _want("v", v, (T, p.Hkv, 64), dt, dev, False)
+    ks, vs, qs = k.stride(), v.stride(), (0, 0)
+    if (q is None) != (q_out is None):
+        _bad("q and q_out go together")
+    if q is not None:
+        _want("q", q, (T, p.H, 64), dt, dev, False)
+        _want("q_out", q_out, (T, p.H, 64), dt, dev)
+        qs = q.stride()
+    if cu_new is not None:
+        _want("cu_new", cu_new, (p.B + 1,), torch.int32, dev)
+    if positions is not None:
+        _want("positions", positions, (1 if rope is None else rope.n_axes, T), torch.int32, dev)
+    strides = (ctypes.c_int64 * 6)(qs[0], qs[1], ks[0], ks[1], vs[0], vs[1])
+    _launch(dev, stream, load().lf_cache_append, ctypes.byref(p), None if rope is None else ctypes.byref(rope), T,
+            _ptr(q), k.data_ptr(), v.data_ptr(), strides, _ptr(cu_new), lengths.data_ptr(), _ptr(positions),
+            block_table.data_ptr(), _ptr(q_out), k_pages.data_ptr(), v_pages.data_ptr(), ws.data_ptr(), ws.numel())
+
+
+def lf_paged_decode(p, q, k_pages, v_pages, block_table, lengths, o, lse, ws, prefix_table=None, stream=None):
+    """Decode step over the paged cache: q [B,H,64] (any strides) against the
+    window of each sequence's own rows and the shared prefix; writes o
+    [B,H,64] and lse [B,H] (or None)."""
+    import torch
+    dt, dev = _paged(p, k_pages, v_pages, block_table, lengths, ws)
+    _want("q", q, (p.B, p.H, 64), dt, dev, False)
+    _want("o", o, (p.B, p.H, 64), dt, dev)
+    if lse is not None:
+        _want("lse", lse, (p.B, p.H), torch.float32, dev)
+    if (prefix_table is None) != (p.prefix_len <= 0):
+        _bad("prefix_table goes with prefix_len > 0")
+    if prefix_table is not None:
+        _want("prefix_table", prefix_table, (-(-p.prefix_len // p.page_size),), torch.int32, dev)
+    qs = q.stride()
+    _launch(dev, stream, load().lf_paged_decode, ctypes.byref(p), q.data_ptr(), (ctypes.c_int64 * 2)(qs[0], qs[1]),
+            k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(), lengths.data_ptr(), _ptr(prefix_table),
+            o.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel())
 
 
 # ------------------------------------------------------------ convenience --
