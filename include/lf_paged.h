@@ -98,9 +98,9 @@ typedef struct lf_paged_params {
 } lf_paged_params;
 
 /* Bytes of device workspace lf_cache_append and lf_paged_decode need (256-byte
- * aligned, its first 32 bytes zeroed once after allocating); 0 on invalid
- * params.  One workspace must not be used by two calls that may run at the
- * same time. */
+ * aligned); 0 on invalid params.  Zero all of it once after allocating; every
+ * call leaves its counters at zero for the next, which may have other params.
+ * One workspace must not be used by two calls that may run at the same time. */
 size_t lf_paged_workspace_size(const lf_paged_params *p);
 
 /* Append T new tokens: K rotated, V as it is, to their rows of the pages, Q

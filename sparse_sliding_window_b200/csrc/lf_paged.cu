@@ -12,22 +12,20 @@
 #include <cooperative_groups.h>
 #include <math.h>
 
-#include "lf_paged.cuh"
+#include "lf_paged_mma.cuh"
 
 namespace cg = cooperative_groups;
 
-__device__ __forceinline__ float lf_exp2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
+// Element (row g, channel c) of the newest token's output from its merged
+// state: o = a / L, lse = log of the sum, 0 and -inf where nothing was attended.
+template <typename T>
+__device__ __forceinline__ void lf_pd_write(T *o, float *lse, size_t row, int c, float M, float L, float a) {
+  const bool none = M == -INFINITY;
+  LfIo1<T>::st(o + row * LF_HD + c, none ? 0.f : a / L);
+  if (lse && c == 0) lse[row] = none ? -INFINITY : (M + log2f(L)) * LF_LN2;
 }
 
-// 2^(m - M), 0 for an empty part (m = -inf), also when everything is empty
-__device__ __forceinline__ float lf_part_scale(float m, float M) {
-  return m == -INFINITY ? 0.f : lf_exp2(m - M);
-}
-
-// ============================================================ decode kernel
+// ===================================================== decode kernel (f32)
 
 #define LF_PD_WARPS 4
 #define LF_PD_LOADS 8  // rows a lane loads per batch
@@ -206,8 +204,7 @@ __global__ void __launch_bounds__(LF_PD_WARPS * 32)
     r_l = cluster.map_shared_rank(c_l, 0);
     r_acc = cluster.map_shared_rank(c_acc, 0);
   }
-  const size_t obase = ((size_t)b * P.H + hk * P.G + g0) * LF_HD;
-  const size_t lbase = (size_t)b * P.H + hk * P.G + g0;
+  const size_t orow = (size_t)b * P.H + hk * P.G + g0;
   for (int e = threadIdx.x; e < GT * LF_HD; e += LF_PD_WARPS * 32) {
     const int g = e / LF_HD, c = e % LF_HD;
     float M = -INFINITY, L = 0.f, a = 0.f;
@@ -226,9 +223,7 @@ __global__ void __launch_bounds__(LF_PD_WARPS * 32)
         r_l[crank * GT + g] = L;
       }
     } else if (g < gn) {
-      const bool none = M == -INFINITY;
-      LfIo1<T>::st(o + obase + e, none ? 0.f : a / L);
-      if (lse && c == 0) lse[lbase + g] = none ? -INFINITY : (M + log2f(L)) * LF_LN2;
+      lf_pd_write(o, lse, orow + g, c, M, L, a);
     }
   }
   if (cl == 1) return;
@@ -243,68 +238,468 @@ __global__ void __launch_bounds__(LF_PD_WARPS * 32)
       L += c_l[r * GT + g] * f;
       a += c_acc[(r * GT + g) * LF_HD + c] * f;
     }
-    const bool none = M == -INFINITY;
-    LfIo1<T>::st(o + obase + e, none ? 0.f : a / L);
-    if (lse && c == 0) lse[lbase + g] = none ? -INFINITY : (M + log2f(L)) * LF_LN2;
+    lf_pd_write(o, lse, orow + g, c, M, L, a);
   }
 }
 
-static cudaLaunchAttribute lf_pdl_attr() {
-  cudaLaunchAttribute a;
-  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  a.val.programmaticStreamSerializationAllowed = 1;
-  return a;
-}
-
-template <typename T, int GT>
-static cudaError_t lf_launch_pd_g(const LfPagedLaunch &L, const void *q, const void *kp,
-                                  const void *vp, void *o, float *lse) {
-  const LfPagedDev &P = L.dev;
-  constexpr int BATCH = 32 / (LF_HD / LfVec<T>::N) * LF_PD_LOADS;
-  const int ngroups = (P.G + GT - 1) / GT;
-  const int64_t units = (int64_t)P.B * P.Hkv * ngroups;
-  // CTAs per unit: enough for four per SM, at most as many as the longest
-  // possible window has work for, and 8 (the portable cluster size)
+// CTAs per unit (sequence, key/value head, query-head group): enough for four
+// per SM, at most as many as the longest possible window has steps of `step`
+// keys, and `most` (a power of two, up to 8, the portable cluster size).
+static int lf_pd_cluster(const LfPagedDev &P, int64_t units, int step, int most) {
   const int64_t cap = (int64_t)P.max_pages << P.shift;
   const int64_t keys = P.window < 0 || P.window >= cap ? cap : P.window + 1;
-  const int64_t work = (keys + BATCH * LF_PD_WARPS - 1) / (BATCH * LF_PD_WARPS);
+  const int64_t work = (keys + step - 1) / step;
   int cl = 1;
-  while (cl < 8 && units * cl < 4 * lf_sm_count() && cl < work) cl *= 2;
+  while (cl < most && units * cl < 4 * lf_sm_count() && cl < work) cl *= 2;
+  return cl;
+}
+
+static cudaError_t lf_pd_launch(const void *fn, const LfPagedLaunch &L, int64_t units, int cl, int smem,
+                                const void *q, const void *kp, const void *vp, void *o, float *lse,
+                                int ngroups) {
   if (units * cl > 0x7fffffff) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(units * cl));
   cfg.blockDim = dim3(LF_PD_WARPS * 32);
-  cfg.dynamicSmemBytes = cl > 1 ? (size_t)cl * GT * (LF_HD + 2) * 4 : 0;
+  cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = L.stream;
   cudaLaunchAttribute attr[2];
-  attr[0] = lf_pdl_attr();
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim.x = (unsigned)cl;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = cl > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, lf_paged_decode_kernel<T, GT>, P, (const T *)q, (const T *)kp,
-                            (const T *)vp, (T *)o, lse, ngroups, cl);
+  void *args[] = {const_cast<LfPagedDev *>(&L.dev), &q, &kp, &vp, &o, &lse, &ngroups, &cl};
+  return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+template <int GT>
+static cudaError_t lf_launch_pd_f32(const LfPagedLaunch &L, const void *q, const void *kp,
+                                    const void *vp, void *o, float *lse) {
+  const LfPagedDev &P = L.dev;
+  constexpr int BATCH = 32 / (LF_HD / LfVec<float>::N) * LF_PD_LOADS;
+  const int ngroups = (P.G + GT - 1) / GT;
+  const int64_t units = (int64_t)P.B * P.Hkv * ngroups;
+  const int cl = lf_pd_cluster(P, units, BATCH * LF_PD_WARPS, 8);
+  return lf_pd_launch((const void *)lf_paged_decode_kernel<float, GT>, L, units, cl,
+                      cl > 1 ? cl * GT * (LF_HD + 2) * 4 : 0, q, kp, vp, o, lse, ngroups);
+}
+
+// Another part (its max, sum and output) into (M, L, a).
+__device__ __forceinline__ void lf_pd_add(float m, float l, float v, float &M, float &L, float &a) {
+  const float N = fmaxf(M, m);
+  const float f = lf_part_scale(M, N), h = lf_part_scale(m, N);
+  M = N;
+  L = L * f + l * h;
+  a = a * f + v * h;
+}
+
+// A fragments of the queries g0 .. g0 + gn - 1 of a key/value head's group;
+// rows behind them repeat the last one and are not written.
+template <typename T, int MT>
+__device__ __forceinline__ void lf_pd_queries(const LfPagedDev &P, const T *q, int b, int hk, int g0, int gn,
+                                              LfPmQ<MT> &qa) {
+  const T *qb = q + b * P.qs[0] + (int64_t)(hk * P.G + g0) * P.qs[1];
+  const int g = threadIdx.x % 32 / 4;
+#pragma unroll
+  for (int mt = 0; mt < MT; mt++)
+    lf_pm_qfrag<T>(qb + min(16 * mt + g, gn - 1) * P.qs[1], qb + min(16 * mt + g + 8, gn - 1) * P.qs[1], qa[mt]);
+}
+
+// Chunks first, first + step, ... of the prefix partials of a row.
+__device__ __forceinline__ void lf_pd_prefix(const LfPagedDev &P, size_t row, int c, int first, int step,
+                                             float &M, float &L, float &a) {
+  const float2 *ml = P.part_ml + row * P.nch;
+  const float *acc = P.part_acc + row * P.nch * LF_HD + c;
+#pragma unroll 4
+  for (int k = first; k < P.nch; k += step) {
+    const float2 x = ml[k];
+    lf_pd_add(x.x, x.y, acc[(size_t)k * LF_HD], M, L, a);
+  }
+}
+
+// ============================= decode kernel (bf16, f16), few sequences
+
+// One cluster of CTAs per (sequence, key/value head, group of 16 MT query
+// heads); its CTAs take the window's tiles of 128 keys in turn, add a share of
+// the prefix partials each, and merge through CTA 0's shared memory.
+template <typename T, int MT>
+__global__ void __launch_bounds__(128, 2)
+    lf_paged_mma_kernel(const __grid_constant__ LfPagedDev P, const T *q, const T *kp, const T *vp, T *o,
+                        float *lse, int ngroups, int cl) {
+  constexpr int RB = 16 * MT;
+  extern __shared__ __align__(16) char smem_raw[];
+  __shared__ float s_m[4][16], s_l[4][16];
+  const bool prefix = P.prefix_len > 0;
+  // Behind a prefix kernel the call's inputs are already complete: every block
+  // of that kernel waited for its own predecessors before it let this one start.
+  if (!prefix) asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  cg::cluster_group cluster = cg::this_cluster();
+  const int crank = cl > 1 ? (int)cluster.block_rank() : 0;
+  const int unit = (int)blockIdx.x / cl;
+  const int gc = unit % ngroups, hk = unit / ngroups % P.Hkv, b = unit / ngroups / P.Hkv;
+  const int g0 = gc * RB, gn = min(RB, P.G - g0);  // query heads of this unit
+  const int len = P.lengths[b];
+  const bool ok = lf_len_ok(len, P.max_pages, P.shift);
+  if (!ok && threadIdx.x == 0 && crank == 0) lf_set_status(P.status, LF_ERR_DEVICE_INPUT, LF_DET_LENGTH + b);
+  const int d = P.dil[hk];
+  const int nk = ok ? lf_window_keys(len, P.window, d) : 0;
+  LfPmQ<MT> qa;
+  lf_pd_queries<T, MT>(P, q, b, hk, g0, gn, qa);
+  LfPmState<MT> S;
+  lf_pm_attend<T, MT>(P, LfPmKeys{P.table + (size_t)b * P.max_pages, P.max_pages, nk, len - 1, -d}, hk,
+                      LF_DET_PAGE + b, kp, vp, crank, cl, qa, (uint32_t)__cvta_generic_to_shared(smem_raw), S);
+
+  // Behind the warps' spilled states [4][16][64], shared memory of CTA 0 holds
+  // the cluster's: acc [cl][gmax][64], m, l [cl][gmax].  The cluster barrier
+  // says that CTA 0 is done with its rings.
+  const int gmax = min(RB, P.G);
+  float *s_acc = reinterpret_cast<float *>(smem_raw);
+  float *c_acc = s_acc + 4 * 16 * LF_HD, *c_m = c_acc + cl * gmax * LF_HD, *c_l = c_m + cl * gmax;
+  __syncthreads();
+  if (cl > 1) cluster.barrier_arrive();
+  if (prefix) asm volatile("griddepcontrol.wait;" ::: "memory");  // the prefix partials
+  float *r_acc = cl > 1 ? cluster.map_shared_rank(c_acc, 0) : nullptr;
+  float *r_m = cl > 1 ? cluster.map_shared_rank(c_m, 0) : nullptr;
+  float *r_l = cl > 1 ? cluster.map_shared_rank(c_l, 0) : nullptr;
+  const size_t orow = (size_t)b * P.H + hk * P.G + g0, prow = ((size_t)hk * P.B + b) * P.G + g0;
+#pragma unroll
+  for (int mt = 0; mt < MT; mt++) {
+    if (mt > 0) __syncthreads();
+    lf_pm_spill<MT>(S, mt, 16, s_acc, s_m, s_l);
+    __syncthreads();
+    if (mt == 0 && cl > 1) cluster.barrier_wait();
+    for (int e = threadIdx.x; e < min(16, gn - 16 * mt) * LF_HD; e += 128) {
+      const int r = e / LF_HD, c = e % LF_HD, x = 16 * mt + r;
+      float M, L, a;
+      lf_pm_merge(16, s_acc, s_m, s_l, r, c, M, L, a);
+      if (prefix && ok) lf_pd_prefix(P, prow + x, c, crank, cl, M, L, a);
+      if (cl > 1) {
+        r_acc[(crank * gmax + x) * LF_HD + c] = a;
+        if (c == 0) {
+          r_m[crank * gmax + x] = M;
+          r_l[crank * gmax + x] = L;
+        }
+      } else {
+        lf_pd_write(o, lse, orow + x, c, M, L, a);
+      }
+    }
+  }
+  if (cl == 1) return;
+  cluster.sync();  // the partials are in CTA 0
+  if (crank != 0) return;
+  for (int e = threadIdx.x; e < gn * LF_HD; e += 128) {
+    const int x = e / LF_HD, c = e % LF_HD;
+    float M = -INFINITY, L = 0.f, a = 0.f;
+    for (int r = 0; r < cl; r++) M = fmaxf(M, c_m[r * gmax + x]);
+    for (int r = 0; r < cl; r++) {
+      const float f = lf_part_scale(c_m[r * gmax + x], M);
+      L += c_l[r * gmax + x] * f;
+      a += c_acc[(r * gmax + x) * LF_HD + c] * f;
+    }
+    lf_pd_write(o, lse, orow + x, c, M, L, a);
+  }
+}
+
+template <typename T, int MT>
+static cudaError_t lf_launch_pd_mma(const LfPagedLaunch &L, const void *q, const void *kp,
+                                    const void *vp, void *o, float *lse) {
+  const LfPagedDev &P = L.dev;
+  constexpr int RB = 16 * MT;
+  const int ngroups = (P.G + RB - 1) / RB, gmax = P.G < RB ? P.G : RB;
+  const int64_t units = (int64_t)P.B * P.Hkv * ngroups;
+  const int cl = lf_pd_cluster(P, units, LF_PM_KEYS, 8);
+  const int merge = 4 * 16 * LF_HD * 4 + cl * gmax * (LF_HD + 2) * 4;
+  const int smem = merge > LF_PM_RING ? merge : LF_PM_RING;
+  const void *fn = (const void *)lf_paged_mma_kernel<T, MT>;
+  const cudaError_t e = lf_kernel_smem(fn, smem);
+  if (e != cudaSuccess) return e;
+  return lf_pd_launch(fn, L, units, cl, smem, q, kp, vp, o, lse, ngroups);
+}
+
+// ============================ decode kernel (bf16, f16), many sequences
+
+// All units' tiles in one list, cut into equal runs, one per CTA: CTAs stay
+// busy to the end whatever the lengths are, and the loads of a CTA's next unit
+// are in flight while it finishes one.  A unit that lies inside a run is
+// written at once; of a unit that is cut, every CTA leaves its part in the
+// workspace and the one that arrives last adds the parts, in the list's order
+// (so the result does not depend on who that is).
+struct LfPdRun {
+  int b, hk, gc;          // unit
+  int tile, nt;           // tile of the unit, its tiles
+  int len, nk, d;
+};
+
+__device__ __forceinline__ int lf_pd_tiles(int nk) {
+  return max(1, (nk + LF_PM_KEYS - 1) / LF_PM_KEYS);  // without keys one empty tile: the output is written all the same
+}
+
+__device__ __forceinline__ void lf_pd_unit(const LfPagedDev &P, const int *s_len, LfPdRun &R) {
+  R.len = s_len[R.b];
+  R.d = P.dil[R.hk];
+  R.nk = lf_window_keys(R.len, P.window, R.d);
+  R.nt = lf_pd_tiles(R.nk);
+}
+
+__device__ __forceinline__ void lf_pd_next(const LfPagedDev &P, const int *s_len, int ngroups, LfPdRun &R) {
+  if (++R.tile < R.nt) return;
+  R.tile = 0;
+  if (++R.gc < ngroups) return;
+  R.gc = 0;
+  if (++R.hk < P.Hkv) {
+    if (P.same_dil) return;
+  } else {
+    R.hk = 0;
+    if (++R.b == P.B) R.b = 0;  // behind the list: not used
+  }
+  lf_pd_unit(P, s_len, R);
+}
+
+template <typename T, int MT>
+__global__ void __launch_bounds__(128, 2)
+    lf_paged_run_kernel(const __grid_constant__ LfPagedDev P, const T *q, const T *kp, const T *vp, T *o,
+                        float *lse, int ngroups, int) {
+  constexpr int RB = 16 * MT;
+  extern __shared__ __align__(16) char smem_raw[];
+  __shared__ float s_m[4][16], s_l[4][16];
+  __shared__ int s_warp[4], s_last;
+  const bool prefix = P.prefix_len > 0;
+  if (!prefix) asm volatile("griddepcontrol.wait;" ::: "memory");  // as in lf_paged_mma_kernel
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int gmax = min(RB, P.G), wrows = min(16, P.G);
+  float *s_acc = reinterpret_cast<float *>(smem_raw + LF_PM_RING);  // [4][wrows][64]
+  int *s_len = reinterpret_cast<int *>(s_acc + 4 * wrows * LF_HD), *s_end = s_len + P.B;
+
+  // tiles up to the end of each sequence
+  int total = 0;
+  for (int b0 = 0; b0 < P.B; b0 += 128) {
+    const int b = b0 + tid;
+    int n = 0;
+    if (b < P.B) {
+      int len = P.lengths[b];
+      if (!lf_len_ok(len, P.max_pages, P.shift)) {
+        if (blockIdx.x == 0) lf_set_status(P.status, LF_ERR_DEVICE_INPUT, LF_DET_LENGTH + b);
+        len = -1;  // attends nothing, not even the prefix
+      }
+      s_len[b] = len;
+      if (P.same_dil) {
+        n = lf_pd_tiles(lf_window_keys(len, P.window, P.dil[0])) * P.Hkv;
+      } else {
+        for (int h = 0; h < P.Hkv; h++) n += lf_pd_tiles(lf_window_keys(len, P.window, P.dil[h]));
+      }
+      n *= ngroups;
+    }
+    int inc = n;
+#pragma unroll
+    for (int w = 1; w < 32; w <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, inc, w);
+      if (lane >= w) inc += x;
+    }
+    if (lane == 31) s_warp[warp] = inc;
+    __syncthreads();
+    int before = total;
+    for (int w = 0; w < 4; w++) {
+      if (w < warp) before += s_warp[w];
+      total += s_warp[w];
+    }
+    if (b < P.B) s_end[b] = before + inc;
+    __syncthreads();
+  }
+
+  // this CTA's run [begin, end) of `total`, cut for n CTAs
+  const int64_t tot = total;
+  const int n = (int)min((int64_t)gridDim.x, max((int64_t)1, tot / LF_PDR_LEAST));
+  const int me = blockIdx.x;
+  if (me < n) {
+    const int begin = (int)(me * tot / n), end = (int)((me + 1) * tot / n);
+    LfPdRun C;
+    int lo = 0, hi = P.B - 1;  // the first sequence that ends behind `begin`
+    while (lo < hi) {
+      const int mid = (lo + hi) / 2;
+      if (s_end[mid] > begin)
+        hi = mid;
+      else
+        lo = mid + 1;
+    }
+    C.b = lo;
+    C.hk = C.gc = 0;
+    int at = begin - (lo > 0 ? s_end[lo - 1] : 0);  // tiles into the sequence
+    for (;;) {
+      lf_pd_unit(P, s_len, C);
+      if (at < C.nt * ngroups) break;
+      at -= C.nt * ngroups;
+      C.hk++;
+    }
+    C.gc = at / C.nt;
+    C.tile = at % C.nt;
+
+    LfPdRun F = C;  // the loader, LF_PM_STAGES - 1 tiles ahead
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem_raw) + warp * LF_PM_STAGES * LF_PM_STAGE;
+    uint32_t have[LF_PM_STAGES] = {};
+    int fill = begin, slot = 0, st = 0;
+    LfPmAhead A;
+    auto lookup = [&]() {
+      lf_pm_lookup(P, LfPmKeys{P.table + (size_t)F.b * P.max_pages, P.max_pages, F.nk, F.len - 1, -F.d}, F.tile,
+                   fill < end, A);
+    };
+    lookup();
+    auto load = [&]() {
+      uint32_t h = 0;
+      if (fill < end) {
+        h = lf_pm_load<T>(P, A, F.hk, LF_DET_PAGE + F.b, kp, vp, ring + slot * LF_PM_STAGE);
+        lf_pd_next(P, s_len, ngroups, F);
+        fill++;
+        lookup();
+      }
+      lf_cp_commit();
+      slot = slot + 1 == LF_PM_STAGES ? 0 : slot + 1;
+      return h;
+    };
+#pragma unroll
+    for (int i = 0; i < LF_PM_STAGES - 1; i++) have[i] = load();
+
+    LfPmQ<MT> qa;
+    LfPmState<MT> S;
+    int first = C.tile;  // first tile of the current unit in this run
+    for (int i = begin; i < end; i++) {
+      const int g0 = C.gc * RB, gn = min(RB, P.G - g0);
+      if (i == begin || C.tile == 0) {
+        lf_pd_queries<T, MT>(P, q, C.b, C.hk, g0, gn, qa);
+        lf_pm_clear<MT>(S);
+        first = C.tile;
+      }
+      lf_cp_wait<LF_PM_STAGES - 2>();
+      __syncwarp();  // the tile is in for every lane, and the stage to fill next has been read
+      have[LF_PM_STAGES - 1] = load();
+      if (have[0]) lf_pm_tile<T, MT>(qa, ring + st * LF_PM_STAGE, have[0], P.scale_log2, S);
+#pragma unroll
+      for (int k = 0; k + 1 < LF_PM_STAGES; k++) have[k] = have[k + 1];
+      st = st + 1 == LF_PM_STAGES ? 0 : st + 1;
+      if (C.tile + 1 == C.nt || i + 1 == end) {
+        const int ustart = i - C.tile, uend = ustart + C.nt;  // the unit in the list
+        const bool whole = first == 0 && C.tile + 1 == C.nt;
+        lf_pm_sum<MT>(S);
+        if (prefix && whole) asm volatile("griddepcontrol.wait;" ::: "memory");  // the prefix partials
+        const size_t orow = (size_t)C.b * P.H + C.hk * P.G + g0;
+        const size_t prow = ((size_t)C.hk * P.B + C.b) * P.G + g0;
+        const size_t mine = (size_t)(2 * me + (first == 0 ? 1 : 0)) * gmax;  // the run's last or first unit
+#pragma unroll
+        for (int mt = 0; mt < MT; mt++) {
+          lf_pm_spill<MT>(S, mt, wrows, s_acc, s_m, s_l);
+          __syncthreads();
+          for (int e = tid; e < min(16, gn - 16 * mt) * LF_HD; e += 128) {
+            const int r = e / LF_HD, c = e % LF_HD, x = 16 * mt + r;
+            float M, L, a;
+            lf_pm_merge(wrows, s_acc, s_m, s_l, r, c, M, L, a);
+            if (whole) {
+              if (prefix && C.len >= 0) lf_pd_prefix(P, prow + x, c, 0, 1, M, L, a);
+              lf_pd_write(o, lse, orow + x, c, M, L, a);
+            } else {
+              P.run_acc[(mine + x) * LF_HD + c] = a;
+              if (c == 0) P.run_ml[mine + x] = make_float2(M, L);
+            }
+          }
+          if (whole || mt + 1 < MT) __syncthreads();  // s_acc, s_m, s_l are free again
+        }
+        if (!whole) {
+          const int unit = (C.b * P.Hkv + C.hk) * ngroups + C.gc;
+          __threadfence();
+          __syncthreads();
+          if (tid == 0) {
+            const int part = C.tile + 1 - first;
+            s_last = atomicAdd(P.run_count + unit, part) + part == C.nt;
+            if (s_last) P.run_count[unit] = 0;  // for the next call
+          }
+          __syncthreads();
+          if (s_last) {
+            __threadfence();
+            if (prefix) asm volatile("griddepcontrol.wait;" ::: "memory");
+            const int c0 = (int)((((int64_t)ustart + 1) * n - 1) / tot), c1 = (int)(((int64_t)uend * n - 1) / tot);
+            for (int e = tid; e < gn * LF_HD; e += 128) {
+              const int x = e / LF_HD, c = e % LF_HD;
+              float M = -INFINITY, L = 0.f, a = 0.f;
+#pragma unroll 4
+              for (int k = c0; k <= c1; k++) {
+                const size_t from = (size_t)(2 * k + (k * tot / n <= ustart ? 1 : 0)) * gmax + x;
+                const float2 ml = __ldcg(P.run_ml + from);
+                lf_pd_add(ml.x, ml.y, __ldcg(P.run_acc + from * LF_HD + c), M, L, a);
+              }
+              if (prefix && C.len >= 0) lf_pd_prefix(P, prow + x, c, 0, 1, M, L, a);
+              lf_pd_write(o, lse, orow + x, c, M, L, a);
+            }
+          }
+        }
+      }
+      lf_pd_next(P, s_len, ngroups, C);
+    }
+    lf_cp_wait<0>();
+  }
+  if (prefix) asm volatile("griddepcontrol.wait;" ::: "memory");  // no block ends before the prefix kernel
+}
+
+static int lf_pdm_rows(const LfPagedDev &P) { return P.G <= 16 ? 16 : 32; }
+
+// Shared memory of the run kernel: rings, spilled states, lengths and ends.
+static int lf_pdr_smem(const LfPagedDev &P) {
+  return LF_PM_RING + 4 * (P.G < 16 ? P.G : 16) * LF_HD * 4 + 2 * P.B * 4;
+}
+
+// CTAs of the run kernel: as many as fit a full B200 at once (two per SM, one
+// where the rings and the lengths leave no room for the second).
+void lf_paged_plan(LfPagedDev &P, int dtype) {
+  P.run_ctas = 0;
+  P.same_dil = 1;
+  for (int h = 1; h < P.Hkv; h++) P.same_dil &= P.dil[h] == P.dil[0];
+  if (dtype == LF_F32 || P.B > LF_PDR_MAX_B) return;
+  const int rb = lf_pdm_rows(P);
+  const int64_t units = (int64_t)P.B * P.Hkv * ((P.G + rb - 1) / rb);
+  const int64_t cap = (int64_t)P.max_pages << P.shift;
+  const int64_t keys = P.window < 0 || P.window >= cap ? cap : P.window + 1;
+  const int64_t tiles = units * ((keys + LF_PM_KEYS - 1) / LF_PM_KEYS);
+  if (units * 8 <= 2 * 148 || units > LF_PDR_MAX_UNITS || tiles >= 1ll << 31) return;
+  const int per = 228 * 1024 / (lf_pdr_smem(P) + 1024 + 640);  // 1 KB of the system's, 640 static
+  const int64_t ctas = 148 * (per < 2 ? per : 2);
+  P.run_ctas = (int)(tiles < ctas ? tiles : ctas);
+}
+
+template <typename T, int MT>
+static cudaError_t lf_launch_pd_run(const LfPagedLaunch &L, const void *q, const void *kp,
+                                    const void *vp, void *o, float *lse) {
+  const LfPagedDev &P = L.dev;
+  constexpr int RB = 16 * MT;
+  const int smem = lf_pdr_smem(P);
+  const void *fn = (const void *)lf_paged_run_kernel<T, MT>;
+  const cudaError_t e = lf_kernel_smem(fn, smem);
+  if (e != cudaSuccess) return e;
+  return lf_pd_launch(fn, L, P.run_ctas, 1, smem, q, kp, vp, o, lse, (P.G + RB - 1) / RB);
 }
 
 template <typename T>
-static cudaError_t lf_launch_pd_t(const LfPagedLaunch &L, const void *q, const void *kp,
-                                  const void *vp, void *o, float *lse) {
-  switch (L.dev.G) {
-    case 1: return lf_launch_pd_g<T, 1>(L, q, kp, vp, o, lse);
-    case 2: return lf_launch_pd_g<T, 2>(L, q, kp, vp, o, lse);
-    default: return lf_launch_pd_g<T, 4>(L, q, kp, vp, o, lse);
-  }
+static cudaError_t lf_launch_pd_16(const LfPagedLaunch &L, const void *q, const void *kp,
+                                   const void *vp, void *o, float *lse) {
+  const bool run = L.dev.run_ctas > 0, small = lf_pdm_rows(L.dev) == 16;
+  if (run) return small ? lf_launch_pd_run<T, 1>(L, q, kp, vp, o, lse) : lf_launch_pd_run<T, 2>(L, q, kp, vp, o, lse);
+  return small ? lf_launch_pd_mma<T, 1>(L, q, kp, vp, o, lse) : lf_launch_pd_mma<T, 2>(L, q, kp, vp, o, lse);
 }
 
 cudaError_t lf_launch_paged_decode(const LfPagedLaunch &L, const void *q, const void *kp,
                                    const void *vp, void *o, float *lse) {
   cudaError_t e;
-  switch (L.dtype) {
-    case LF_F32: e = lf_launch_pd_t<float>(L, q, kp, vp, o, lse); break;
-    case LF_BF16: e = lf_launch_pd_t<__nv_bfloat16>(L, q, kp, vp, o, lse); break;
-    default: e = lf_launch_pd_t<__half>(L, q, kp, vp, o, lse);
-  }
+  if (L.dtype == LF_BF16)
+    e = lf_launch_pd_16<__nv_bfloat16>(L, q, kp, vp, o, lse);
+  else if (L.dtype == LF_F16)
+    e = lf_launch_pd_16<__half>(L, q, kp, vp, o, lse);
+  else if (L.dev.G == 1)
+    e = lf_launch_pd_f32<1>(L, q, kp, vp, o, lse);
+  else if (L.dev.G == 2)
+    e = lf_launch_pd_f32<2>(L, q, kp, vp, o, lse);
+  else
+    e = lf_launch_pd_f32<4>(L, q, kp, vp, o, lse);
   if (e == cudaSuccess) lf_launches_add(1);
   return e;
 }

@@ -60,14 +60,23 @@ struct LfPagedDev {
   int32_t *status;
   float *part_acc;       // [Hkv * B * G][nch][64]
   float2 *part_ml;       // [Hkv * B * G][nch]
+  // decode over many sequences: CTAs (0: not used), their parts and counters
+  int run_ctas, same_dil;
+  float *run_acc;        // [2 * run_ctas][min(G, 32)][64]
+  float2 *run_ml;        // [2 * run_ctas][min(G, 32)]
+  int32_t *run_count;    // [units], zero between calls
   int dil[LF_MAX_H];     // per key/value head
 };
+
+#define LF_PDR_MAX_UNITS 32768  // units with a counter
+#define LF_PDR_MAX_B 1024  // sequences whose lengths the decode kernel keeps in shared memory
+#define LF_PDR_LEAST 2     // tiles a CTA takes at least
 
 cudaError_t lf_launch_rope(const LfRopeArgs &a, int dtype, bool append, cudaStream_t stream);
 
 struct LfPagedLaunch {
   LfPagedDev dev;
-  size_t off_acc, off_ml, total;  // workspace
+  size_t off_acc, off_ml, off_run_acc, off_run_ml, total;  // workspace
   int dtype;
   cudaStream_t stream;
 };
@@ -77,3 +86,5 @@ cudaError_t lf_launch_paged_decode(const LfPagedLaunch &L, const void *q, const 
 cudaError_t lf_launch_prefix(const LfPagedLaunch &L, const void *q, const void *kp, const void *vp);
 // chunks and keys per chunk of the prefix split
 void lf_prefix_plan(LfPagedDev &d, int dtype);
+// run_ctas and same_dil
+void lf_paged_plan(LfPagedDev &d, int dtype);

@@ -148,6 +148,8 @@ extern "C" int lf_rope_bwd(const lf_rope_params *r, int B, int n, int dtype, int
 
 // --------------------------------------------------------------- paged cache
 
+#define LP_OFF_COUNT 256  // counters of the decode kernel, behind the status words
+
 static size_t lp_align(size_t x) { return (x + 255) & ~(size_t)255; }
 
 static int lp_prepare(const lf_paged_params *p, LfPagedLaunch &L) {
@@ -190,11 +192,19 @@ static int lp_prepare(const lf_paged_params *p, LfPagedLaunch &L) {
   d.scale_log2 = (p->scale > 0.f ? p->scale : 1.f / sqrtf((float)LF_HD)) * LF_LOG2E;
   lf_prefix_plan(d, p->dtype);
   const size_t parts = (size_t)p->B * p->H * d.nch;
-  size_t off = lp_align(LF_ST_WORDS * 4);
+  // the counters have the same place whatever the params are, so that one
+  // zeroed workspace serves calls with different params
+  size_t off = LP_OFF_COUNT + LF_PDR_MAX_UNITS * 4;
   L.off_acc = off;
   off = lp_align(off + parts * LF_HD * 4);
   L.off_ml = off;
   off = lp_align(off + parts * 8);
+  lf_paged_plan(d, p->dtype);
+  const size_t rows = d.run_ctas ? 2 * (size_t)d.run_ctas * (d.G < 32 ? d.G : 32) : 0;
+  L.off_run_acc = off;
+  off = lp_align(off + rows * LF_HD * 4);
+  L.off_run_ml = off;
+  off = lp_align(off + rows * 8);
   L.total = off;
   L.dtype = p->dtype;
   return LF_OK;
@@ -214,6 +224,9 @@ static int lp_bind(const lf_paged_params *p, void *workspace, size_t ws_bytes, v
   L.dev.status = (int32_t *)ws;
   L.dev.part_acc = (float *)(ws + L.off_acc);
   L.dev.part_ml = (float2 *)(ws + L.off_ml);
+  L.dev.run_acc = (float *)(ws + L.off_run_acc);
+  L.dev.run_ml = (float2 *)(ws + L.off_run_ml);
+  L.dev.run_count = (int32_t *)(ws + LP_OFF_COUNT);
   L.stream = (cudaStream_t)stream;
   return LF_OK;
 }

@@ -20,17 +20,22 @@ LF_PAGES_FN bool lf_len_ok(int len, int columns, int shift) {
   return len >= 0 && len <= (columns << shift);
 }
 
-// Pool row of cache row `row` for key/value head h: the pools are
-// [num_pages, Hkv, page_size] rows of 64.  num_pages * Hkv * page_size < 2^31
-// and columns * page_size <= 2^30 hold on entry, so nothing overflows.
-LF_PAGES_FN int lf_pool_row(const int32_t *table, int columns, int num_pages, int shift, int Hkv,
-                            int h, int row) {
-  if (row < 0) return LF_ROW_NONE;
-  const int col = row >> shift;
-  if (col >= columns) return LF_ROW_NONE;
-  const int page = table[col];
+// Is cache row `row` inside its table?
+LF_PAGES_FN bool lf_row_ok(int columns, int shift, int row) { return row >= 0 && (row >> shift) < columns; }
+
+// Pool row of cache row `row`, which lies in `page`, for key/value head h: the
+// pools are [num_pages, Hkv, page_size] rows of 64.  num_pages * Hkv *
+// page_size < 2^31 holds on entry, so nothing overflows.
+LF_PAGES_FN int lf_row_in_page(int page, int num_pages, int shift, int Hkv, int h, int row) {
   if (page < 0 || page >= num_pages) return LF_ROW_BAD;
   return ((page * Hkv + h) << shift) + (row & ((1 << shift) - 1));
+}
+
+// The two together, through the table (columns * page_size <= 2^30).
+LF_PAGES_FN int lf_pool_row(const int32_t *table, int columns, int num_pages, int shift, int Hkv,
+                            int h, int row) {
+  if (!lf_row_ok(columns, shift, row)) return LF_ROW_NONE;
+  return lf_row_in_page(table[row >> shift], num_pages, shift, Hkv, h, row);
 }
 
 // Keys that the newest token of a sequence of length len attends among its

@@ -326,35 +326,45 @@ def _bad(msg: str):
     raise LfError(LF_ERR_INVALID, msg)
 
 
-def _want(name: str, t, shape, dtype, dev, packed: bool = True):
-    """t is a CUDA tensor of this shape, dtype and device; packed: contiguous,
-    else only its last dimension."""
+def _want(name: str, t, shape, dtype, dev: int, packed: bool = True):
+    """t is a tensor of this shape and dtype on CUDA device `dev`; packed:
+    contiguous, else only its last dimension."""
+    if t.shape == shape and t.dtype is dtype and t.get_device() == dev and (
+            t.is_contiguous() or not packed and t.stride(-1) == 1):
+        return t.data_ptr()
     if t.shape != shape:
         _bad("%s has shape %s, %s is wanted" % (name, tuple(t.shape), tuple(shape)))
     if t.dtype is not dtype:
         _bad("%s is %s, %s is wanted" % (name, t.dtype, dtype))
-    if t.device != dev:
-        _bad("%s is on %s, the call on %s" % (name, t.device, dev))
-    if not t.is_contiguous() and (packed or t.stride(-1) != 1):
-        _bad("%s is not contiguous%s" % (name, "" if packed else " in its last dimension"))
+    if t.get_device() != dev:
+        _bad("%s is on %s, the call on cuda:%d" % (name, t.device, dev))
+    _bad("%s is not contiguous%s" % (name, "" if packed else " in its last dimension"))
 
 
-def _cuda_device(t, name: str):
+def _cuda_device(t, name: str) -> int:
     if not t.is_cuda:
         _bad("%s is not on a GPU" % name)
-    return t.device
+    return t.get_device()
 
 
-def _launch(dev, stream, fn, *args):
-    """fn(*args, stream) with dev as the current device; stream None: dev's current stream."""
+def _launch(dev: int, stream, fn, *args):
+    """fn(*args, stream) with CUDA device `dev` current; stream None: its
+    current stream (its raw handle: building the Stream object costs 3 us, as
+    much as the launch)."""
     import torch
-    if stream is not None and stream.device != dev:
-        _bad("the stream is on %s, the tensors on %s" % (stream.device, dev))
-    if torch.cuda.current_device() == dev.index:
-        _check(fn(*args, (stream or torch.cuda.current_stream(dev)).cuda_stream))
-        return
-    with torch.cuda.device(dev):
-        _check(fn(*args, (stream or torch.cuda.current_stream(dev)).cuda_stream))
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(dev)
+    elif stream.device_index != dev:
+        _bad("the stream is on %s, the tensors on cuda:%d" % (stream.device, dev))
+    else:
+        handle = stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev:
+        code = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            code = fn(*args, handle)
+    if code:
+        _check(code)
 
 
 def _torch_dtype(code: int):
@@ -368,6 +378,9 @@ def _dtype_of(t, name: str) -> int:
     if code is None:
         _bad("%s is %s: float32, bfloat16 or float16 is wanted" % (name, t.dtype))
     return code
+
+
+_I64x2, _I64x6 = ctypes.c_int64 * 2, ctypes.c_int64 * 6
 
 
 def make_rope_params(rot_dim: int = 64, interleaved: bool = False, n_axes: int = 1,
@@ -390,23 +403,22 @@ def _rope(fn, r, xs, outs, positions, stream):
     if not 1 <= len(xs) <= 8 or len(outs) != len(xs):
         _bad("1 to 8 tensors are wanted, and an output for each")
     first = xs[0]
-    dev, code = _cuda_device(first, "x"), _dtype_of(first, "x")
+    dev, code, dt = _cuda_device(first, "x"), _dtype_of(first, "x"), first.dtype
     if first.dim() != 4:
         _bad("x has %d dimensions, [B, heads, n, 64] is wanted" % first.dim())
     B, _, n, _ = first.shape
-    arr = (lf_rope_tensor * len(xs))()
-    for t, x, out in zip(arr, xs, outs):
+    tensors = []
+    for x, out in zip(xs, outs):
         if x.dim() != 4:
             _bad("x has %d dimensions, [B, heads, n, 64] is wanted" % x.dim())
-        shape = (B, x.shape[1], n, 64)
-        _want("x", x, shape, first.dtype, dev, False)
-        _want("out", out, shape, first.dtype, dev, False)
-        t.x, t.out, t.heads = x.data_ptr(), out.data_ptr(), shape[1]
-        t.x_stride[:], t.out_stride[:] = x.stride()[:3], out.stride()[:3]
+        heads = x.shape[1]
+        shape = (B, heads, n, 64)
+        tensors.append((_want("x", x, shape, dt, dev, False), _want("out", out, shape, dt, dev, False), heads,
+                        x.stride()[:3], out.stride()[:3]))
     if positions is not None:
         import torch
-        _want("positions", positions, (r.n_axes, B, n), torch.int32, dev)
-    _launch(dev, stream, fn, ctypes.byref(r), B, n, code, len(xs), arr, _ptr(positions))
+        positions = _want("positions", positions, (r.n_axes, B, n), torch.int32, dev)
+    _launch(dev, stream, fn, ctypes.byref(r), B, n, code, len(xs), (lf_rope_tensor * len(xs))(*tensors), positions)
 
 
 def lf_rope_fwd(r, xs, outs, positions=None, stream=None):
@@ -451,20 +463,20 @@ def paged_workspace(p, device="cuda"):
 
 
 def _paged(p, k_pages, v_pages, block_table, lengths, ws):
-    """The checks that append and decode share; returns (torch dtype, device)."""
+    """The checks that append and decode share; returns (dtype, device, the
+    pointers of the pools, the table and the lengths)."""
     import torch
-    dev = _cuda_device(k_pages, "k_pages")
-    if p.dtype not in (LF_F32, LF_BF16, LF_F16):
-        _bad("bad dtype %d" % p.dtype)
-    dt = _torch_dtype(p.dtype)
-    pool = (p.num_pages, p.Hkv, p.page_size, p.head_dim)
-    _want("k_pages", k_pages, pool, dt, dev)
-    _want("v_pages", v_pages, pool, dt, dev)
-    _want("block_table", block_table, (p.B, p.max_pages), torch.int32, dev)
-    _want("lengths", lengths, (p.B,), torch.int32, dev)
-    if ws.dtype is not torch.uint8 or ws.device != dev or not ws.is_contiguous():
-        _bad("the workspace is a contiguous uint8 tensor on %s" % dev)
-    return dt, dev
+    dev, i32 = _cuda_device(k_pages, "k_pages"), torch.int32
+    code, B, hkv = p.dtype, p.B, p.Hkv
+    if not 0 <= code <= 2:
+        _bad("bad dtype %d" % code)
+    dt = _torch_dtype(code)
+    pool = (p.num_pages, hkv, p.page_size, 64)
+    ptrs = (_want("k_pages", k_pages, pool, dt, dev), _want("v_pages", v_pages, pool, dt, dev),
+            _want("block_table", block_table, (B, p.max_pages), i32, dev), _want("lengths", lengths, (B,), i32, dev))
+    if ws.dtype is not torch.uint8 or ws.get_device() != dev or not ws.is_contiguous():
+        _bad("the workspace is a contiguous uint8 tensor on cuda:%d" % dev)
+    return dt, dev, B, hkv, ptrs
 
 
 def lf_cache_append(p, rope, q, k, v, lengths, block_table, q_out, k_pages, v_pages, ws, cu_new=None,
@@ -473,25 +485,28 @@ def lf_cache_append(p, rope, q, k, v, lengths, block_table, q_out, k_pages, v_pa
     [T,Hkv,64], any strides (a projection's [1,H,T,64] is x[0].transpose(0, 1));
     K rotated by rope (None: not) and V go to the pages, rotated Q to q_out."""
     import torch
-    dt, dev = _paged(p, k_pages, v_pages, block_table, lengths, ws)
+    dt, dev, B, hkv, (kp, vp, table, lens) = _paged(p, k_pages, v_pages, block_table, lengths, ws)
     T = k.shape[0]
-    _want("k", k, (T, p.Hkv, 64), dt, dev, False)
-    _want("v", v, (T, p.Hkv, 64), dt, dev, False)
-    ks, vs, qs = k.stride(), v.stride(), (0, 0)
+    kv = (T, hkv, 64)
+    kq = _want("k", k, kv, dt, dev, False)
+    vq = _want("v", v, kv, dt, dev, False)
+    qp = qo = None
+    qs = ks = k.stride()
+    vs = v.stride()
     if (q is None) != (q_out is None):
         _bad("q and q_out go together")
     if q is not None:
-        _want("q", q, (T, p.H, 64), dt, dev, False)
-        _want("q_out", q_out, (T, p.H, 64), dt, dev)
+        heads = (T, p.H, 64)
+        qp = _want("q", q, heads, dt, dev, False)
+        qo = _want("q_out", q_out, heads, dt, dev)
         qs = q.stride()
     if cu_new is not None:
-        _want("cu_new", cu_new, (p.B + 1,), torch.int32, dev)
+        cu_new = _want("cu_new", cu_new, (B + 1,), torch.int32, dev)
     if positions is not None:
-        _want("positions", positions, (1 if rope is None else rope.n_axes, T), torch.int32, dev)
-    strides = (ctypes.c_int64 * 6)(qs[0], qs[1], ks[0], ks[1], vs[0], vs[1])
+        positions = _want("positions", positions, (1 if rope is None else rope.n_axes, T), torch.int32, dev)
     _launch(dev, stream, load().lf_cache_append, ctypes.byref(p), None if rope is None else ctypes.byref(rope), T,
-            _ptr(q), k.data_ptr(), v.data_ptr(), strides, _ptr(cu_new), lengths.data_ptr(), _ptr(positions),
-            block_table.data_ptr(), _ptr(q_out), k_pages.data_ptr(), v_pages.data_ptr(), ws.data_ptr(), ws.numel())
+            qp, kq, vq, _I64x6(qs[0], qs[1], ks[0], ks[1], vs[0], vs[1]), cu_new, lens, positions, table, qo, kp, vp,
+            ws.data_ptr(), ws.numel())
 
 
 def lf_paged_decode(p, q, k_pages, v_pages, block_table, lengths, o, lse, ws, prefix_table=None, stream=None):
@@ -499,19 +514,20 @@ def lf_paged_decode(p, q, k_pages, v_pages, block_table, lengths, o, lse, ws, pr
     window of each sequence's own rows and the shared prefix; writes o
     [B,H,64] and lse [B,H] (or None)."""
     import torch
-    dt, dev = _paged(p, k_pages, v_pages, block_table, lengths, ws)
-    _want("q", q, (p.B, p.H, 64), dt, dev, False)
-    _want("o", o, (p.B, p.H, 64), dt, dev)
+    dt, dev, B, _, (kp, vp, table, lens) = _paged(p, k_pages, v_pages, block_table, lengths, ws)
+    H = p.H
+    rows = (B, H, 64)
+    qp, op = _want("q", q, rows, dt, dev, False), _want("o", o, rows, dt, dev)
     if lse is not None:
-        _want("lse", lse, (p.B, p.H), torch.float32, dev)
-    if (prefix_table is None) != (p.prefix_len <= 0):
+        lse = _want("lse", lse, (B, H), torch.float32, dev)
+    prefix = p.prefix_len
+    if (prefix_table is None) != (prefix <= 0):
         _bad("prefix_table goes with prefix_len > 0")
-    if prefix_table is not None:
-        _want("prefix_table", prefix_table, (-(-p.prefix_len // p.page_size),), torch.int32, dev)
-    qs = q.stride()
-    _launch(dev, stream, load().lf_paged_decode, ctypes.byref(p), q.data_ptr(), (ctypes.c_int64 * 2)(qs[0], qs[1]),
-            k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(), lengths.data_ptr(), _ptr(prefix_table),
-            o.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel())
+    if prefix > 0:
+        prefix_table = _want("prefix_table", prefix_table, (-(-prefix // p.page_size),), torch.int32, dev)
+    _launch(dev, stream, load().lf_paged_decode, ctypes.byref(p), qp,
+            None if q.is_contiguous() else _I64x2(*q.stride()[:2]), kp, vp, table, lens, prefix_table, op, lse,
+            ws.data_ptr(), ws.numel())
 
 
 # ------------------------------------------------------------ convenience --

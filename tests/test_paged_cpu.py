@@ -132,9 +132,9 @@ GOOD = dict(B=2, H=4, Hkv=2, page_size=16, num_pages=9, max_pages=4, window=5, d
 
 def test_workspace_sizes(lib):
     small = L.lf_paged_workspace_size(L.make_paged_params(**GOOD))
-    assert small == 256
+    assert small > 0 and small % 256 == 0
     more = L.lf_paged_workspace_size(L.make_paged_params(**{**GOOD, "prefix_len": 1000}))
-    assert more >= 256 + 2 * 4 * (64 + 2) * 4 and more % 256 == 0
+    assert more >= small + 2 * 4 * (64 + 2) * 4 and more % 256 == 0
     for bad in (dict(B=0), dict(H=0), dict(Hkv=0), dict(Hkv=3), dict(H=256, Hkv=2), dict(page_size=8), dict(page_size=24),
                 dict(page_size=2048), dict(num_pages=0), dict(max_pages=0), dict(dtype=3), dict(prefix_len=-1),
                 dict(prefix_len=2 ** 30 + 1), dict(head_dim=128), dict(scale=-1.0), dict(scale=float("nan")),
@@ -155,7 +155,7 @@ def test_decode_and_append_refusals(lib):
     p = L.make_paged_params(**GOOD)
     pp = ctypes.byref(p)
 
-    def decode(par=pp, q=a, st=None, kp=a, vp=a, table=a, lens=a, pre=None, o=a, lse=None, ws=a, n=4096):
+    def decode(par=pp, q=a, st=None, kp=a, vp=a, table=a, lens=a, pre=None, o=a, lse=None, ws=a, n=1 << 30):
         return lib.lf_paged_decode(par, q, st, kp, vp, table, lens, pre, o, lse, ws, n, None)
 
     for kw in (dict(par=None), dict(q=None), dict(q=a + 2), dict(kp=None), dict(vp=a + 8), dict(table=None), dict(table=a + 1),
@@ -163,11 +163,11 @@ def test_decode_and_append_refusals(lib):
                dict(st=(ctypes.c_int64 * 2)(-64, 64)), dict(st=(ctypes.c_int64 * 2)(256, 65))):
         assert decode(**kw) == L.LF_ERR_INVALID, kw
     pre = L.make_paged_params(**{**GOOD, "prefix_len": 100})
-    assert decode(par=ctypes.byref(pre), n=1 << 30) == L.LF_ERR_INVALID and b"prefix_table" in lib.lf_attn_last_error()
+    assert decode(par=ctypes.byref(pre)) == L.LF_ERR_INVALID and b"prefix_table" in lib.lf_attn_last_error()
     wide = L.make_paged_params(**{**GOOD, "head_dim": 128})
     assert decode(par=ctypes.byref(wide)) == L.LF_ERR_UNSUPPORTED
 
-    def append(par=pp, rope=None, T=2, q=a, k=a, v=a, st=None, cu=None, lens=a, pos=None, table=a, qo=a, kp=a, vp=a, ws=a, n=4096):
+    def append(par=pp, rope=None, T=2, q=a, k=a, v=a, st=None, cu=None, lens=a, pos=None, table=a, qo=a, kp=a, vp=a, ws=a, n=1 << 30):
         return lib.lf_cache_append(par, rope, T, q, k, v, st, cu, lens, pos, table, qo, kp, vp, ws, n, None)
 
     two = ctypes.byref(L.make_rope_params(n_axes=2, pair_axis=[0, 1] * 16))

@@ -107,6 +107,13 @@ DECODE = [
     (8, 8, 64, [2600], 512, [2, 2, 1, 1, 1, 1, 1, 1]),
     (12, 12, 16, [40 + 7 * b for b in range(70)], 64, None),
     (2, 2, 16, [50, 50], 2 ** 31 - 1, [2 ** 31 - 1, 7]),
+    # many sequences: units cut between blocks, one much longer than the rest
+    (4, 2, 16, [(b * 37) % 130 for b in range(60)] + [2000], -1, None),
+    (4, 4, 32, [(b * 53) % 400 for b in range(30)], 100, [1, 2, 3, 1]),
+    (20, 1, 16, [(b * 11) % 90 for b in range(80)], -1, None),
+    (40, 1, 64, [b % 70 for b in range(80)], 30, None),
+    (96, 1, 16, [b % 40 for b in range(41)], -1, None),
+    (1, 1, 16, [b % 19 for b in range(1100)], -1, None),
 ]
 
 
@@ -129,6 +136,9 @@ PREFIX = [
     (12, 12, 64, [b % 50 for b in range(70)], 16, 515),
     (8, 2, 16, [b % 5 for b in range(40)], -1, 200),
     (16, 2, 1024, [3] * 33, -1, 1100),
+    (4, 2, 16, [(b * 37) % 130 for b in range(60)] + [1500], -1, 90),
+    (24, 1, 32, [b % 40 for b in range(80)], 10, 200),
+    (48, 1, 16, [b % 20 for b in range(80)], -1, 33),
 ]
 
 
@@ -214,8 +224,10 @@ def test_decode_leaves_out_bad_pages_and_lengths(dtype, prefix):
         got, gl = call(c.t_table, c.t_lengths, pre, "prefix table")
         none = Cache(51, dtype, 3, 2, 16, lengths, prefix)
         none.prefix, none.prefix_table = 0, none.prefix_table[:0]
-        ro, rl, to, tl = _reference(none, q, H, -1, None, 0.125, 0.0)
-        R.check("o", R.f64(got), ro, to + R.half_step(dtype) * (np.abs(ro) + to) + 1e-30)
+        # 16-bit probabilities enter the product with V rounded: sum_j p_j (1 + e_j) v_j with |e_j| <= half a
+        # step is off by at most half_step * sum_j p_j |v_j|, the last argument's part of the allowance
+        ro, rl, to, tl = _reference(none, q, H, -1, None, 0.125, R.half_step(dtype) if dtype != "f32" else 0.0)
+        R.check("o", R.f64(got), ro, to + 2.0 ** -22 + R.half_step(dtype) * (np.abs(ro) + to))
 
 
 def test_decode_captured_and_two_graphs_share_a_workspace():
@@ -259,6 +271,30 @@ def test_decode_captured_and_two_graphs_share_a_workspace():
     L.lf_paged_decode(*args(qs[0], outs[0]), stream=side)
     side.synchronize()
     assert torch.equal(outs[0][0], want[0][0])
+
+
+def test_decode_calls_with_other_params_share_a_workspace():
+    """One zeroed workspace for calls of different batches and heads, each
+    repeated: the same bits every time, and those of a fresh workspace."""
+    import torch
+    runs = []
+    for k, (H, Hkv, lengths, prefix) in enumerate([(4, 2, [(b * 29) % 300 for b in range(64)], 0), (12, 3, [900] * 30, 50),
+                                                   (2, 2, [5, 700], 130), (40, 1, [77] * 90, 0)]):
+        c = Cache(510 + k, "bf16", len(lengths), Hkv, 16, lengths, prefix)
+        runs.append((c, c.params(H), _normal(c.rng, (len(lengths), H, 64), "bf16")))
+    ws = torch.zeros(max(L.lf_paged_workspace_size(p) for _, p, _ in runs), dtype=torch.uint8, device="cuda")
+
+    def once(c, p, q, w):
+        o, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+        L.lf_paged_decode(p, q, c.k, c.v, c.t_table, c.t_lengths, o, lse, w, prefix_table=c.t_prefix)
+        return o, lse
+
+    want = [once(*r, L.paged_workspace(r[1])) for r in runs]
+    for _ in range(3):
+        for r, w in zip(runs, want):
+            got = once(*r, ws)
+            assert torch.equal(got[0], w[0]) and torch.equal(got[1], w[1])
+    L.lf_attn_status(ws)
 
 
 # ------------------------------------------------------------------- append --
