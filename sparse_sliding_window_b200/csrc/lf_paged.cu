@@ -459,8 +459,37 @@ __device__ __forceinline__ void lf_pd_next(const LfPagedDev &P, const int *s_len
   lf_pd_unit(P, s_len, R);
 }
 
+// The unit that holds tile t of the list, and t's tile of it.
+__device__ __forceinline__ void lf_pd_find(const LfPagedDev &P, const int *s_len, const int *s_end, int ngroups,
+                                           int t, LfPdRun &R) {
+  int lo = 0, hi = P.B - 1;  // the first sequence that ends behind t
+  while (lo < hi) {
+    const int mid = (lo + hi) / 2;
+    if (s_end[mid] > t)
+      hi = mid;
+    else
+      lo = mid + 1;
+  }
+  R.b = lo;
+  R.hk = 0;
+  int at = t - (lo > 0 ? s_end[lo - 1] : 0);  // tiles into the sequence
+  for (;;) {
+    lf_pd_unit(P, s_len, R);
+    const int head = R.nt * ngroups;
+    if (P.same_dil) {
+      R.hk = at / head;
+      at %= head;
+    }
+    if (at < head) break;
+    at -= head;
+    R.hk++;
+  }
+  R.gc = at / R.nt;
+  R.tile = at % R.nt;
+}
+
 template <typename T, int MT>
-__global__ void __launch_bounds__(128, 2)
+__global__ void __launch_bounds__(128, MT == 1 ? 3 : 2)
     lf_paged_run_kernel(const __grid_constant__ LfPagedDev P, const T *q, const T *kp, const T *vp, T *o,
                         float *lse, int ngroups, int) {
   constexpr int RB = 16 * MT;
@@ -516,27 +545,24 @@ __global__ void __launch_bounds__(128, 2)
   const int n = (int)min((int64_t)gridDim.x, max((int64_t)1, tot / LF_PDR_LEAST));
   const int me = blockIdx.x;
   if (me < n) {
-    const int begin = (int)(me * tot / n), end = (int)((me + 1) * tot / n);
+    // Cuts k tot / n; one that falls into a short unit moves to the nearer of
+    // its ends (handing the parts of a unit over costs as much as some tiles).
     LfPdRun C;
-    int lo = 0, hi = P.B - 1;  // the first sequence that ends behind `begin`
-    while (lo < hi) {
-      const int mid = (lo + hi) / 2;
-      if (s_end[mid] > begin)
-        hi = mid;
-      else
-        lo = mid + 1;
+    auto cut = [&](int k) {
+      const int t = (int)(k * tot / n);
+      if (t >= total) return total;
+      lf_pd_find(P, s_len, s_end, ngroups, t, C);
+      return C.nt > LF_PDR_WHOLE ? t : 2 * C.tile < C.nt ? t - C.tile : t - C.tile + C.nt;
+    };
+    const int end = cut(me + 1), begin = cut(me);
+    if (begin < end && C.nt <= LF_PDR_WHOLE) {  // to the unit that starts at begin
+      if (2 * C.tile < C.nt) {
+        C.tile = 0;
+      } else {
+        C.tile = C.nt - 1;
+        lf_pd_next(P, s_len, ngroups, C);
+      }
     }
-    C.b = lo;
-    C.hk = C.gc = 0;
-    int at = begin - (lo > 0 ? s_end[lo - 1] : 0);  // tiles into the sequence
-    for (;;) {
-      lf_pd_unit(P, s_len, C);
-      if (at < C.nt * ngroups) break;
-      at -= C.nt * ngroups;
-      C.hk++;
-    }
-    C.gc = at / C.nt;
-    C.tile = at % C.nt;
 
     LfPdRun F = C;  // the loader, LF_PM_STAGES - 1 tiles ahead
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem_raw) + warp * LF_PM_STAGES * LF_PM_STAGE;
@@ -663,7 +689,8 @@ void lf_paged_plan(LfPagedDev &P, int dtype) {
   const int64_t tiles = units * ((keys + LF_PM_KEYS - 1) / LF_PM_KEYS);
   if (units * 8 <= 2 * 148 || units > LF_PDR_MAX_UNITS || tiles >= 1ll << 31) return;
   const int per = 228 * 1024 / (lf_pdr_smem(P) + 1024 + 640);  // 1 KB of the system's, 640 static
-  const int64_t ctas = 148 * (per < 2 ? per : 2);
+  const int most = rb == 16 ? 3 : 2;
+  const int64_t ctas = 148 * (per < most ? per : most);
   P.run_ctas = (int)(tiles < ctas ? tiles : ctas);
 }
 

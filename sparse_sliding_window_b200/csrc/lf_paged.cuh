@@ -71,6 +71,7 @@ struct LfPagedDev {
 #define LF_PDR_MAX_UNITS 32768  // units with a counter
 #define LF_PDR_MAX_B 1024  // sequences whose lengths the decode kernel keeps in shared memory
 #define LF_PDR_LEAST 2     // tiles a CTA takes at least
+#define LF_PDR_WHOLE 6     // units up to so many tiles are not cut
 
 cudaError_t lf_launch_rope(const LfRopeArgs &a, int dtype, bool append, cudaStream_t stream);
 

@@ -19,7 +19,7 @@
 #define LF_PM_KEYS 128                   // keys per tile, 32 per warp
 #define LF_PM_HALF (32 * LF_HD * 2)      // bytes of a warp's K (or V) rows of a tile
 #define LF_PM_STAGE (2 * LF_PM_HALF)
-#define LF_PM_STAGES 3
+#define LF_PM_STAGES 2
 #define LF_PM_RING (4 * LF_PM_STAGES * LF_PM_STAGE)  // bytes of the four warps' rings
 
 __device__ __forceinline__ float lf_exp2(float x) {
