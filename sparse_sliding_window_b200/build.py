@@ -13,7 +13,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "liblf_attn.so")
 SOURCES = ["lf_api.cu", "lf_simt.cu", "lf_tc.cu", "lf_tc_bwd.cu", "lf_static.cu", "lf_gemm.cu",
-           "lf_rope.cu", "lf_paged.cu", "lf_prefix.cu", "lf_paged_api.cu"]
+           "lf_rope.cu", "lf_paged.cu", "lf_prefix.cu", "lf_prefix_tc.cu", "lf_paged_api.cu"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",

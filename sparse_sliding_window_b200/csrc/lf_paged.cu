@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(LF_PD_WARPS * 32)
       for (int j = 0; j < N; j++) acc[g][j] *= f;
 #pragma unroll
       for (int i = 0; i < LF_PD_LOADS; i++) {
-        s[g][i] = (have >> i & 1) ? lf_exp2(s[g][i] - M) : 0.f;
+        s[g][i] = (have >> i & 1) ? lf_ex2(s[g][i] - M) : 0.f;
         l[g] += s[g][i];
       }
     }
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(LF_PD_WARPS * 32)
             *reinterpret_cast<float4 *>(a + j) = *reinterpret_cast<const float4 *>(P.part_acc + at * LF_HD + lr * N + j);
           if (ml.x == -INFINITY) continue;
           const float M = fmaxf(m[g], ml.x);
-          const float f = lf_part_scale(m[g], M), e = lf_exp2(ml.x - M);
+          const float f = lf_part_scale(m[g], M), e = lf_ex2(ml.x - M);
           m[g] = M;
           l[g] = l[g] * f + ml.y * e;
 #pragma unroll

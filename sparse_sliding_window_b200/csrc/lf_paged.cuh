@@ -49,7 +49,7 @@ struct LfRopeArgs {
   int32_t *status;
 };
 
-// Split of the shared prefix: its keys in `nch` chunks of `chunk`.
+// nch: parts that the prefix kernel leaves per row; chunk: keys a block takes.
 struct LfPagedDev {
   int B, H, Hkv, G;      // G = H / Hkv
   int shift, num_pages, max_pages;
@@ -85,7 +85,10 @@ struct LfPagedLaunch {
 cudaError_t lf_launch_paged_decode(const LfPagedLaunch &L, const void *q, const void *kp,
                                    const void *vp, void *o, float *lse);
 cudaError_t lf_launch_prefix(const LfPagedLaunch &L, const void *q, const void *kp, const void *vp);
-// chunks and keys per chunk of the prefix split
+// parts and keys per chunk of the prefix split
 void lf_prefix_plan(LfPagedDev &d, int dtype);
+// the same of the tensor-core kernel (bf16, f16, more than 32 rows)
+cudaError_t lf_launch_prefix_tc(const LfPagedLaunch &L, const void *q, const void *kp, const void *vp);
+void lf_prefix_tc_plan(LfPagedDev &d);
 // run_ctas and same_dil
 void lf_paged_plan(LfPagedDev &d, int dtype);

@@ -15,6 +15,7 @@
 #include <type_traits>
 
 #include "lf_paged.cuh"
+#include "lf_ptx.cuh"
 
 #define LF_PM_KEYS 128                   // keys per tile, 32 per warp
 #define LF_PM_HALF (32 * LF_HD * 2)      // bytes of a warp's K (or V) rows of a tile
@@ -22,15 +23,9 @@
 #define LF_PM_STAGES 2
 #define LF_PM_RING (4 * LF_PM_STAGES * LF_PM_STAGE)  // bytes of the four warps' rings
 
-__device__ __forceinline__ float lf_exp2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // 2^(m - M), 0 for an empty part (m = -inf), also when everything is empty
 __device__ __forceinline__ float lf_part_scale(float m, float M) {
-  return m == -INFINITY ? 0.f : lf_exp2(m - M);
+  return m == -INFINITY ? 0.f : lf_ex2(m - M);
 }
 
 // 16 bytes to shared memory, zeros when !take (src is then not read)
@@ -207,10 +202,10 @@ __device__ __forceinline__ void lf_pm_tile(const LfPmQ<MT> &qa, uint32_t sk, uin
     const float e0 = M0 == -INFINITY ? 0.f : M0, e1 = M1 == -INFINITY ? 0.f : M1;
 #pragma unroll
     for (int n = 0; n < 4; n++) {
-      s[mt][n][0] = lf_exp2(fmaf(s[mt][n][0], scale_log2, -e0));
-      s[mt][n][1] = lf_exp2(fmaf(s[mt][n][1], scale_log2, -e0));
-      s[mt][n][2] = lf_exp2(fmaf(s[mt][n][2], scale_log2, -e1));
-      s[mt][n][3] = lf_exp2(fmaf(s[mt][n][3], scale_log2, -e1));
+      s[mt][n][0] = lf_ex2(fmaf(s[mt][n][0], scale_log2, -e0));
+      s[mt][n][1] = lf_ex2(fmaf(s[mt][n][1], scale_log2, -e0));
+      s[mt][n][2] = lf_ex2(fmaf(s[mt][n][2], scale_log2, -e1));
+      s[mt][n][3] = lf_ex2(fmaf(s[mt][n][3], scale_log2, -e1));
       S.l[mt][0] += s[mt][n][0] + s[mt][n][1];
       S.l[mt][1] += s[mt][n][2] + s[mt][n][3];
     }

@@ -96,13 +96,13 @@ __global__ void __launch_bounds__(256) lf_prefix_simt_kernel(const __grid_consta
         if (ok[i]) M = fmaxf(M, s[u][i]);
 #pragma unroll
       for (int w = 8; w > 0; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
-      const float f = m[u] == -INFINITY ? 0.f : lf_exp2(m[u] - M);
+      const float f = m[u] == -INFINITY ? 0.f : lf_ex2(m[u] - M);
       m[u] = M;
       l[u] *= f;
 #pragma unroll
       for (int i = 0; i < 4; i++) {
         acc[u][i] *= f;
-        const float p = ok[i] ? lf_exp2(s[u][i] - M) : 0.f;
+        const float p = ok[i] ? lf_ex2(s[u][i] - M) : 0.f;
         l[u] += p;
         S.p[r + 16 * u][c + 16 * i] = p;
       }
@@ -178,6 +178,10 @@ __global__ void __launch_bounds__(128, 2) lf_prefix_mma_kernel(const __grid_cons
 
 // ----------------------------------------------------------------- launches
 
+// The tensor-core kernel's tile has 128 rows: it takes over where the rows no
+// longer fit one block of the warp-level kernel.
+static bool lf_prefix_is_tc(const LfPagedDev &d, int dtype) { return dtype != LF_F32 && (int64_t)d.B * d.G > 32; }
+
 static int lf_prefix_rows(const LfPagedDev &d, int dtype) {
   if (dtype == LF_F32) return LF_PXS_ROWS;
   return d.B * d.G <= 16 ? 16 : 32;
@@ -190,6 +194,7 @@ void lf_prefix_plan(LfPagedDev &d, int dtype) {
   d.nch = 0;
   d.chunk = 0;
   if (d.prefix_len <= 0) return;
+  if (lf_prefix_is_tc(d, dtype)) return lf_prefix_tc_plan(d);
   const int rb = lf_prefix_rows(d, dtype);
   const int64_t blocks = (int64_t)d.Hkv * ((d.B * d.G + rb - 1) / rb);
   const int keys = dtype == LF_F32 ? LF_PX_KEYS : LF_PM_KEYS;  // of a tile
@@ -234,6 +239,8 @@ cudaError_t lf_launch_prefix(const LfPagedLaunch &L, const void *q, const void *
   cudaError_t e;
   if (L.dtype == LF_F32)
     e = lf_px_launch((const void *)lf_prefix_simt_kernel, L, LF_PXS_ROWS, 256, (int)sizeof(LfPxsSmem), q, kp, vp);
+  else if (lf_prefix_is_tc(L.dev, L.dtype))
+    e = lf_launch_prefix_tc(L, q, kp, vp);
   else if (L.dtype == LF_BF16)
     e = lf_launch_prefix_t<__nv_bfloat16>(L, q, kp, vp);
   else
