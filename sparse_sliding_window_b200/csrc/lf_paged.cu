@@ -154,11 +154,11 @@ __global__ void __launch_bounds__(LF_PD_WARPS * 32)
         for (int g = 0; g < GT; g++) {
           if (g >= gn) continue;
           const size_t at = (rows + g) * P.nch + c;
-          const float2 ml = P.part_ml[at];
+          const float2 ml = __ldcg(P.part_ml + at);
           float a[N];
 #pragma unroll
           for (int j = 0; j < N; j += 4)
-            *reinterpret_cast<float4 *>(a + j) = *reinterpret_cast<const float4 *>(P.part_acc + at * LF_HD + lr * N + j);
+            *reinterpret_cast<float4 *>(a + j) = __ldcg(reinterpret_cast<const float4 *>(P.part_acc + at * LF_HD + lr * N + j));
           if (ml.x == -INFINITY) continue;
           const float M = fmaxf(m[g], ml.x);
           const float f = lf_part_scale(m[g], M), e = lf_ex2(ml.x - M);
@@ -308,16 +308,90 @@ __device__ __forceinline__ void lf_pd_queries(const LfPagedDev &P, const T *q, i
     lf_pm_qfrag<T>(qb + min(16 * mt + g, gn - 1) * P.qs[1], qb + min(16 * mt + g + 8, gn - 1) * P.qs[1], qa[mt]);
 }
 
-// Chunks first, first + step, ... of the prefix partials of a row.
+// Parts first, first + step, ... that the prefix kernel left of a row.  The
+// parts are read past L1 (here and below): an earlier call's may still be there.
 __device__ __forceinline__ void lf_pd_prefix(const LfPagedDev &P, size_t row, int c, int first, int step,
                                              float &M, float &L, float &a) {
   const float2 *ml = P.part_ml + row * P.nch;
   const float *acc = P.part_acc + row * P.nch * LF_HD + c;
 #pragma unroll 4
   for (int k = first; k < P.nch; k += step) {
-    const float2 x = ml[k];
-    lf_pd_add(x.x, x.y, acc[(size_t)k * LF_HD], M, L, a);
+    const float2 x = __ldcg(ml + k);
+    lf_pd_add(x.x, x.y, __ldcg(acc + (size_t)k * LF_HD), M, L, a);
   }
+}
+
+// All parts of up to 16 rows, by a block of 128 threads: the weights of a
+// row's parts first (8 lanes a row), then their weighted sum with 16 bytes a
+// load and every load independent of the others; rows few enough leave
+// several threads to an element, whose sums lf_pd_folded adds.  (One thread
+// per element that added part after part took 8 us of the 26 us that the
+// decode kernel needs behind a prefix with 22 parts for 64 sequences x 12
+// heads.)
+struct LfPdFold {
+  float *w;    // [rows][nch]
+  float2 *ml;  // [16]
+  float *sum;  // [threads per element][rows][64]
+};
+__host__ __device__ __forceinline__ int lf_pd_fold_ways(int rows) { return rows == 1 ? 8 : rows == 2 ? 4 : rows <= 4 ? 2 : 1; }
+__host__ __device__ __forceinline__ int lf_pd_fold_bytes(int rows, int nch) {  // multiple of 16
+  return 16 * 8 + (rows * nch + 3) / 4 * 16 + (rows < 8 ? 8 : rows) * LF_HD * 4;
+}
+__device__ __forceinline__ LfPdFold lf_pd_fold_at(char *smem, int rows, int nch) {
+  LfPdFold F;
+  F.ml = reinterpret_cast<float2 *>(smem);
+  F.w = reinterpret_cast<float *>(smem + 16 * 8);
+  F.sum = F.w + (rows * nch + 3) / 4 * 4;
+  return F;
+}
+__device__ __forceinline__ void lf_pd_fold(const LfPagedDev &P, size_t row0, int rows, const LfPdFold &F) {
+  const int tid = threadIdx.x, nch = P.nch;
+  {
+    const int x = tid / 8, s = tid % 8;
+    float2 v[LF_PART_MAX / 8];
+    float M = -INFINITY, L = 0.f;
+#pragma unroll
+    for (int i = 0; i < LF_PART_MAX / 8; i++) {
+      const int k = s + 8 * i;
+      v[i] = x < rows && k < nch ? __ldcg(P.part_ml + (row0 + x) * nch + k) : make_float2(-INFINITY, 0.f);
+      M = fmaxf(M, v[i].x);
+    }
+#pragma unroll
+    for (int w = 1; w < 8; w <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
+#pragma unroll
+    for (int i = 0; i < LF_PART_MAX / 8; i++) {
+      const int k = s + 8 * i;
+      const float f = lf_part_scale(v[i].x, M);
+      L += v[i].y * f;
+      if (x < rows && k < nch) F.w[x * nch + k] = f;
+    }
+#pragma unroll
+    for (int w = 1; w < 8; w <<= 1) L += __shfl_xor_sync(0xffffffffu, L, w);
+    if (s == 0 && x < rows) F.ml[x] = make_float2(M, L);
+  }
+  __syncthreads();
+  const int ways = lf_pd_fold_ways(rows), c = tid % 16 * 4;
+  for (int item = tid / 16; item < rows * ways; item += 8) {
+    const int x = item % rows, sub = item / rows;
+    const float *acc = P.part_acc + (row0 + x) * nch * LF_HD + c, *w = F.w + x * nch;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = sub; k < nch; k += ways) {
+      const float4 v = __ldcg(reinterpret_cast<const float4 *>(acc + (size_t)k * LF_HD));
+      a.x = fmaf(w[k], v.x, a.x);
+      a.y = fmaf(w[k], v.y, a.y);
+      a.z = fmaf(w[k], v.z, a.z);
+      a.w = fmaf(w[k], v.w, a.w);
+    }
+    *reinterpret_cast<float4 *>(F.sum + (sub * rows + x) * LF_HD + c) = a;
+  }
+  __syncthreads();
+}
+// Channel c of row x of the fold, added to (M, L, a).
+__device__ __forceinline__ void lf_pd_folded(const LfPdFold &F, int rows, int x, int c, float &M, float &L, float &a) {
+  float v = 0.f;
+  for (int sub = 0; sub < lf_pd_fold_ways(rows); sub++) v += F.sum[(sub * rows + x) * LF_HD + c];
+  lf_pd_add(F.ml[x].x, F.ml[x].y, v, M, L, a);
 }
 
 // ============================= decode kernel (bf16, f16), few sequences
@@ -502,7 +576,10 @@ __global__ void __launch_bounds__(128, MT == 1 ? 3 : 2)
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int gmax = min(RB, P.G), wrows = min(16, P.G);
   float *s_acc = reinterpret_cast<float *>(smem_raw + LF_PM_RING);  // [4][wrows][64]
-  int *s_len = reinterpret_cast<int *>(s_acc + 4 * wrows * LF_HD), *s_end = s_len + P.B;
+  const LfPdFold fold = lf_pd_fold_at(smem_raw + LF_PM_RING + 4 * wrows * LF_HD * 4, wrows, P.nch);
+  int *s_len = reinterpret_cast<int *>(s_acc + 4 * wrows * LF_HD);
+  if (prefix) s_len += lf_pd_fold_bytes(wrows, P.nch) / 4;
+  int *s_end = s_len + P.B;
 
   // tiles up to the end of each sequence
   int total = 0;
@@ -616,14 +693,17 @@ __global__ void __launch_bounds__(128, MT == 1 ? 3 : 2)
         const size_t mine = (size_t)(2 * me + (first == 0 ? 1 : 0)) * gmax;  // the run's last or first unit
 #pragma unroll
         for (int mt = 0; mt < MT; mt++) {
+          const int nr = min(16, gn - 16 * mt);
+          const bool folds = prefix && whole && C.len >= 0 && nr > 0;
           lf_pm_spill<MT>(S, mt, wrows, s_acc, s_m, s_l);
+          if (folds) lf_pd_fold(P, prow + 16 * mt, nr, fold);
           __syncthreads();
-          for (int e = tid; e < min(16, gn - 16 * mt) * LF_HD; e += 128) {
+          for (int e = tid; e < nr * LF_HD; e += 128) {
             const int r = e / LF_HD, c = e % LF_HD, x = 16 * mt + r;
             float M, L, a;
             lf_pm_merge(wrows, s_acc, s_m, s_l, r, c, M, L, a);
             if (whole) {
-              if (prefix && C.len >= 0) lf_pd_prefix(P, prow + x, c, 0, 1, M, L, a);
+              if (folds) lf_pd_folded(fold, nr, r, c, M, L, a);
               lf_pd_write(o, lse, orow + x, c, M, L, a);
             } else {
               P.run_acc[(mine + x) * LF_HD + c] = a;
@@ -646,17 +726,23 @@ __global__ void __launch_bounds__(128, MT == 1 ? 3 : 2)
             __threadfence();
             if (prefix) asm volatile("griddepcontrol.wait;" ::: "memory");
             const int c0 = (int)((((int64_t)ustart + 1) * n - 1) / tot), c1 = (int)(((int64_t)uend * n - 1) / tot);
-            for (int e = tid; e < gn * LF_HD; e += 128) {
-              const int x = e / LF_HD, c = e % LF_HD;
-              float M = -INFINITY, L = 0.f, a = 0.f;
+            for (int x0 = 0; x0 < gn; x0 += 16) {
+              const int nr = min(16, gn - x0);
+              const bool folds = prefix && C.len >= 0;
+              if (folds) lf_pd_fold(P, prow + x0, nr, fold);
+              for (int e = tid; e < nr * LF_HD; e += 128) {
+                const int r = e / LF_HD, c = e % LF_HD, x = x0 + r;
+                float M = -INFINITY, L = 0.f, a = 0.f;
 #pragma unroll 4
-              for (int k = c0; k <= c1; k++) {
-                const size_t from = (size_t)(2 * k + (k * tot / n <= ustart ? 1 : 0)) * gmax + x;
-                const float2 ml = __ldcg(P.run_ml + from);
-                lf_pd_add(ml.x, ml.y, __ldcg(P.run_acc + from * LF_HD + c), M, L, a);
+                for (int k = c0; k <= c1; k++) {
+                  const size_t from = (size_t)(2 * k + (k * tot / n <= ustart ? 1 : 0)) * gmax + x;
+                  const float2 ml = __ldcg(P.run_ml + from);
+                  lf_pd_add(ml.x, ml.y, __ldcg(P.run_acc + from * LF_HD + c), M, L, a);
+                }
+                if (folds) lf_pd_folded(fold, nr, r, c, M, L, a);
+                lf_pd_write(o, lse, orow + x, c, M, L, a);
               }
-              if (prefix && C.len >= 0) lf_pd_prefix(P, prow + x, c, 0, 1, M, L, a);
-              lf_pd_write(o, lse, orow + x, c, M, L, a);
+              __syncthreads();
             }
           }
         }
@@ -670,9 +756,10 @@ __global__ void __launch_bounds__(128, MT == 1 ? 3 : 2)
 
 static int lf_pdm_rows(const LfPagedDev &P) { return P.G <= 16 ? 16 : 32; }
 
-// Shared memory of the run kernel: rings, spilled states, lengths and ends.
+// Shared memory of the run kernel: rings, spilled states, prefix fold, lengths and ends.
 static int lf_pdr_smem(const LfPagedDev &P) {
-  return LF_PM_RING + 4 * (P.G < 16 ? P.G : 16) * LF_HD * 4 + 2 * P.B * 4;
+  const int wrows = P.G < 16 ? P.G : 16;
+  return LF_PM_RING + 4 * wrows * LF_HD * 4 + (P.nch > 0 ? lf_pd_fold_bytes(wrows, P.nch) : 0) + 2 * P.B * 4;
 }
 
 // CTAs of the run kernel: as many as fit a full B200 at once (two per SM, one

@@ -68,6 +68,7 @@ struct LfPagedDev {
   int dil[LF_MAX_H];     // per key/value head
 };
 
+#define LF_PART_MAX 64          // parts per row at most
 #define LF_PDR_MAX_UNITS 32768  // units with a counter
 #define LF_PDR_MAX_B 1024  // sequences whose lengths the decode kernel keeps in shared memory
 #define LF_PDR_LEAST 2     // tiles a CTA takes at least

@@ -200,7 +200,7 @@ void lf_prefix_plan(LfPagedDev &d, int dtype) {
   const int keys = dtype == LF_F32 ? LF_PX_KEYS : LF_PM_KEYS;  // of a tile
   const int tiles = (d.prefix_len + keys - 1) / keys;
   int64_t want = (4 * 148 + blocks - 1) / blocks;
-  if (want > 64) want = 64;
+  if (want > LF_PART_MAX) want = LF_PART_MAX;
   if (want > tiles) want = tiles;
   const int per = (int)((tiles + want - 1) / want);
   d.chunk = per * keys;

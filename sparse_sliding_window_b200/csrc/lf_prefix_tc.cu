@@ -435,7 +435,7 @@ void lf_prefix_tc_plan(LfPagedDev &d) {
   const int64_t blocks = (int64_t)d.Hkv * (((int64_t)d.B * d.G + LF_PT_ROWS - 1) / LF_PT_ROWS);
   int64_t want = 148 / blocks;
   if (want < 1) want = 1;
-  if (want > 32) want = 32;
+  if (want > LF_PART_MAX / 2) want = LF_PART_MAX / 2;
   if (want > tiles) want = tiles;
   const int per = (int)((tiles + want - 1) / want);
   d.chunk = per * LF_PT_KEYS;
