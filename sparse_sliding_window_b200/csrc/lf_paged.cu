@@ -533,34 +533,35 @@ __device__ __forceinline__ void lf_pd_next(const LfPagedDev &P, const int *s_len
   lf_pd_unit(P, s_len, R);
 }
 
-// The unit that holds tile t of the list, and t's tile of it.
-__device__ __forceinline__ void lf_pd_find(const LfPagedDev &P, const int *s_len, const int *s_end, int ngroups,
-                                           int t, LfPdRun &R) {
-  int lo = 0, hi = P.B - 1;  // the first sequence that ends behind t
-  while (lo < hi) {
-    const int mid = (lo + hi) / 2;
-    if (s_end[mid] > t)
-      hi = mid;
-    else
-      lo = mid + 1;
-  }
-  R.b = lo;
+// The unit that holds the at-th tile of sequence b, and the tile of it.
+__device__ __forceinline__ void lf_pd_find(const LfPagedDev &P, const int *s_len, int ngroups, int b, int at,
+                                           LfPdRun &R) {
+  R.b = b;
   R.hk = 0;
-  int at = t - (lo > 0 ? s_end[lo - 1] : 0);  // tiles into the sequence
   for (;;) {
     lf_pd_unit(P, s_len, R);
     const int head = R.nt * ngroups;
-    if (P.same_dil) {
+    if (P.same_dil && P.Hkv > 1) {
       R.hk = at / head;
-      at %= head;
+      at -= R.hk * head;
     }
     if (at < head) break;
     at -= head;
     R.hk++;
   }
-  R.gc = at / R.nt;
-  R.tile = at % R.nt;
+  R.gc = ngroups > 1 ? at / R.nt : 0;
+  R.tile = at - R.gc * R.nt;
 }
+
+// The list of `total` tiles is cut for n CTAs: per or per + 1 tiles each.
+struct LfPdCuts {
+  int n, per, more;  // the first `more` CTAs have one tile more
+  __device__ __forceinline__ int at(int k) const { return k * per + min(k, more); }
+  __device__ __forceinline__ int cta_of(int t) const {
+    const int longer = more * (per + 1);
+    return t < longer ? t / (per + 1) : more + (t - longer) / per;
+  }
+};
 
 template <typename T, int MT>
 __global__ void __launch_bounds__(128, MT == 1 ? 3 : 2)
@@ -569,7 +570,8 @@ __global__ void __launch_bounds__(128, MT == 1 ? 3 : 2)
   constexpr int RB = 16 * MT;
   extern __shared__ __align__(16) char smem_raw[];
   __shared__ float s_m[4][16], s_l[4][16];
-  __shared__ int s_warp[4], s_last;
+  __shared__ int s_warp[4], s_last, s_at[2];
+  __shared__ LfPdRun s_cut[2];
   const bool prefix = P.prefix_len > 0;
   if (!prefix) asm volatile("griddepcontrol.wait;" ::: "memory");  // as in lf_paged_mma_kernel
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -617,29 +619,49 @@ __global__ void __launch_bounds__(128, MT == 1 ? 3 : 2)
     __syncthreads();
   }
 
-  // this CTA's run [begin, end) of `total`, cut for n CTAs
-  const int64_t tot = total;
-  const int n = (int)min((int64_t)gridDim.x, max((int64_t)1, tot / LF_PDR_LEAST));
+  // This CTA's run [begin, end): a cut that falls into a short unit moves to
+  // the nearer of its ends (handing the parts of a unit over costs as much as
+  // some tiles).  Lanes 0 and 1 of warp 0 find the two cuts' units.
+  LfPdCuts cuts;
+  cuts.n = min((int)gridDim.x, max(1, total / LF_PDR_LEAST));
+  cuts.per = total / cuts.n;
+  cuts.more = total - cuts.per * cuts.n;
   const int me = blockIdx.x;
-  if (me < n) {
-    // Cuts k tot / n; one that falls into a short unit moves to the nearer of
-    // its ends (handing the parts of a unit over costs as much as some tiles).
-    LfPdRun C;
-    auto cut = [&](int k) {
-      const int t = (int)(k * tot / n);
-      if (t >= total) return total;
-      lf_pd_find(P, s_len, s_end, ngroups, t, C);
-      return C.nt > LF_PDR_WHOLE ? t : 2 * C.tile < C.nt ? t - C.tile : t - C.tile + C.nt;
-    };
-    const int end = cut(me + 1), begin = cut(me);
-    if (begin < end && C.nt <= LF_PDR_WHOLE) {  // to the unit that starts at begin
-      if (2 * C.tile < C.nt) {
-        C.tile = 0;
-      } else {
-        C.tile = C.nt - 1;
-        lf_pd_next(P, s_len, ngroups, C);
+  if (me < cuts.n) {
+    for (int b = tid; b < P.B; b += 128) {
+      const int b0 = b > 0 ? s_end[b - 1] : 0, b1 = s_end[b];
+#pragma unroll
+      for (int k = 0; k < 2; k++) {
+        const int t = cuts.at(me + k);
+        if (t >= b0 && t < b1) {
+          s_cut[k].b = b;
+          s_cut[k].tile = t - b0;
+        }
       }
     }
+    __syncthreads();
+    LfPdRun C;
+    if (tid < 2) {
+      int t = cuts.at(me + tid);
+      if (t < total) {
+        lf_pd_find(P, s_len, ngroups, s_cut[tid].b, s_cut[tid].tile, C);
+        if (C.nt <= LF_PDR_WHOLE) {
+          t -= C.tile;
+          if (2 * C.tile < C.nt) {
+            C.tile = 0;
+          } else {
+            t += C.nt;
+            C.tile = C.nt - 1;
+            lf_pd_next(P, s_len, ngroups, C);
+          }
+        }
+        s_cut[tid] = C;
+      }
+      s_at[tid] = t;
+    }
+    __syncthreads();
+    C = s_cut[0];
+    const int begin = s_at[0], end = s_at[1];
 
     LfPdRun F = C;  // the loader, LF_PM_STAGES - 1 tiles ahead
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem_raw) + warp * LF_PM_STAGES * LF_PM_STAGE;
@@ -725,7 +747,7 @@ __global__ void __launch_bounds__(128, MT == 1 ? 3 : 2)
           if (s_last) {
             __threadfence();
             if (prefix) asm volatile("griddepcontrol.wait;" ::: "memory");
-            const int c0 = (int)((((int64_t)ustart + 1) * n - 1) / tot), c1 = (int)(((int64_t)uend * n - 1) / tot);
+            const int c0 = cuts.cta_of(ustart), c1 = cuts.cta_of(uend - 1);
             for (int x0 = 0; x0 < gn; x0 += 16) {
               const int nr = min(16, gn - x0);
               const bool folds = prefix && C.len >= 0;
@@ -735,7 +757,7 @@ __global__ void __launch_bounds__(128, MT == 1 ? 3 : 2)
                 float M = -INFINITY, L = 0.f, a = 0.f;
 #pragma unroll 4
                 for (int k = c0; k <= c1; k++) {
-                  const size_t from = (size_t)(2 * k + (k * tot / n <= ustart ? 1 : 0)) * gmax + x;
+                  const size_t from = (size_t)(2 * k + (cuts.at(k) <= ustart ? 1 : 0)) * gmax + x;
                   const float2 ml = __ldcg(P.run_ml + from);
                   lf_pd_add(ml.x, ml.y, __ldcg(P.run_acc + from * LF_HD + c), M, L, a);
                 }

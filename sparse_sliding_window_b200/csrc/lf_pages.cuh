@@ -43,7 +43,7 @@ LF_PAGES_FN int lf_pool_row(const int32_t *table, int columns, int num_pages, in
 LF_PAGES_FN int lf_window_keys(int len, int window, int d) {
   if (len <= 0) return 0;
   if (window < 0) return len;
-  const int last = (len - 1) / d;
+  const int last = d == 1 ? len - 1 : (len - 1) / d;
   return (window < last ? window : last) + 1;
 }
 
