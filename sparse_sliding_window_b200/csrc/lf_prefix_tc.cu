@@ -56,6 +56,10 @@ static_assert(LF_PT_SMEM <= 232448, "shared memory per CTA");
 // A row's reference may lag its running maximum by this much (log2): p stays
 // below 2^8 and O is rescaled only when a score is far above everything before.
 #define LF_PT_LAG 8.f
+// One pair of exponentials in so many goes to the FMA pipe: the special
+// function unit takes 8 cycles for a warp's 32, the rest of the work leaves
+// the FMA pipe half idle.
+#define LF_PT_FMA_EXP 0
 
 // Warp-uniform bounded wait, inlined: the softmax warps hold a row of S in
 // registers across it, which a call would push to local memory.
@@ -91,6 +95,70 @@ __device__ __forceinline__ void lf_pt_drain(uint32_t bar, uint32_t parity, int32
       break;
     }
   }
+}
+
+// ---- pairs of float32 in one 64-bit register (sm_100 packed arithmetic)
+typedef unsigned long long LfPair;
+__device__ __forceinline__ LfPair lf_pair(float a, float b) {
+  LfPair r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ LfPair lf_pair_u(uint32_t a, uint32_t b) {
+  LfPair r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ void lf_unpair(LfPair p, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
+}
+__device__ __forceinline__ LfPair lf_fma2(LfPair a, LfPair b, LfPair c) {
+  LfPair r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ LfPair lf_add2(LfPair a, LfPair b) {
+  LfPair r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ LfPair lf_mul2(LfPair a, LfPair b) {
+  LfPair r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float lf_max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float lf_max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// 2^x of a pair on the FMA pipe, x <= 2^8 or NaN: x = n + f with n the nearest
+// integer (adding 1.5 * 2^23 leaves n in the low bits), 2^f on [-1/2, 1/2] by
+// the polynomial of degree 5 of least largest relative error (fitted by
+// iterated reweighted least squares: 7.5e-8, 2.2e-7 with float32 roundings;
+// ex2.approx: 2 units in the last place), times 2^n made from its bits.
+// Results below 2^-126 come out as about 2^-126; NaN stays NaN.
+__device__ __forceinline__ LfPair lf_exp2_fma(LfPair x) {
+  float a, b;
+  lf_unpair(x, a, b);
+  x = lf_pair(lf_max_nan(a, -126.f), lf_max_nan(b, -126.f));
+  const LfPair t = lf_add2(x, lf_pair(12582912.f, 12582912.f));
+  const LfPair n = lf_add2(t, lf_pair(-12582912.f, -12582912.f));
+  const LfPair f = lf_fma2(n, lf_pair(-1.f, -1.f), x);
+  LfPair r = lf_fma2(lf_pair(1.3276461e-3f, 1.3276461e-3f), f, lf_pair(9.675541e-3f, 9.675541e-3f));
+  r = lf_fma2(r, f, lf_pair(5.5507135e-2f, 5.5507135e-2f));
+  r = lf_fma2(r, f, lf_pair(0.2402212f, 0.2402212f));
+  r = lf_fma2(r, f, lf_pair(0.69314694f, 0.69314694f));
+  r = lf_fma2(r, f, lf_pair(1.0000001f, 1.0000001f));
+  float ta, tb;
+  lf_unpair(t, ta, tb);
+  return lf_mul2(r, lf_pair_u((__float_as_uint(ta) << 23) + 0x3f800000u, (__float_as_uint(tb) << 23) + 0x3f800000u));
 }
 
 struct LfPtParams {
@@ -309,17 +377,19 @@ __global__ void __launch_bounds__(LF_PT_THREADS, 1) lf_prefix_tc_kernel(const __
         if (!ok) break;
         const uint4 mask = *reinterpret_cast<const uint4 *>(misc + LF_PT_MASK + 16 * s);
         const uint32_t w[4] = {mask.x, mask.y, mask.z, mask.w};
-        float mx[4];
+        const bool all = (w[0] & w[1] & w[2] & w[3]) == 0xffffffffu;
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        if (all) {
 #pragma unroll
-        for (int k = 0; k < 4; k++) {
-          mx[k] = -INFINITY;
-          if (w[k] == 0xffffffffu) {
+          for (int e = 0; e < 32; e += 2)
 #pragma unroll
-            for (int e = 0; e < 32; e++) mx[k] = fmaxf(mx[k], __uint_as_float(v[k][e]));
-          } else {
+            for (int k = 0; k < 4; k++)
+              mx[k] = lf_max3(mx[k], __uint_as_float(v[k][e]), __uint_as_float(v[k][e + 1]));
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; k++)
 #pragma unroll
             for (int e = 0; e < 32; e++) mx[k] = fmaxf(mx[k], (w[k] >> e & 1u) ? __uint_as_float(v[k][e]) : -INFINITY);
-          }
         }
         const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
         if (fresh && (w[0] | w[1] | w[2] | w[3]) != 0u) {
@@ -344,41 +414,54 @@ __global__ void __launch_bounds__(LF_PT_THREADS, 1) lf_prefix_tc_kernel(const __
             lf_tmem_st16(tO + e, ov);
           }
         }
+        if (!waited) {  // the stream's last product has read P
+          ok = lf_pt_wait(bar + LF_PT_PV_DONE(g), (c - 1) & 1, abort_flag, P.status, 52);
+          if (!ok) break;
+          lf_tc_fence_after();
+        }
         // P is rounded to the 16-bit type for the product with V (p < 2^8,
         // half a step relative each); the row sum keeps the unrounded values
-        float sum0 = 0.f, sum1 = 0.f;
+        if (all) {
+          LfPair sums[2] = {lf_pair(0.f, 0.f), lf_pair(0.f, 0.f)};
+          const LfPair sl2p = lf_pair(sl2, sl2), refp = lf_pair(-m_ref, -m_ref);
 #pragma unroll
-        for (int k = 0; k < 4; k++) {
-          uint32_t pw[16];
-          if (w[k] == 0xffffffffu) {
+          for (int k = 0; k < 4; k++) {
+            uint32_t pw[16];
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-              const float p0 = lf_ex2(fmaf(__uint_as_float(v[k][e]), sl2, -m_ref));
-              const float p1 = lf_ex2(fmaf(__uint_as_float(v[k][e + 1]), sl2, -m_ref));
-              sum0 += p0;
-              sum1 += p1;
+              LfPair x2 = lf_fma2(lf_pair_u(v[k][e], v[k][e + 1]), sl2p, refp);
+              float p0, p1;
+              if (LF_PT_FMA_EXP && e / 2 % LF_PT_FMA_EXP == LF_PT_FMA_EXP - 1) {
+                x2 = lf_exp2_fma(x2);
+                lf_unpair(x2, p0, p1);
+              } else {
+                lf_unpair(x2, p0, p1);
+                p0 = lf_ex2(p0);
+                p1 = lf_ex2(p1);
+                x2 = lf_pair(p0, p1);
+              }
+              sums[e / 2 % 2] = lf_add2(sums[e / 2 % 2], x2);
               pw[e / 2] = lf_pack2<kF16>(p0, p1);
             }
-          } else {
+            lf_tmem_st16(tP + 16 * k, pw);
+          }
+          float s0, s1;
+          lf_unpair(lf_add2(sums[0], sums[1]), s0, s1);
+          l += s0 + s1;
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; k++) {
+            uint32_t pw[16];
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
               const float p0 = (w[k] >> e & 1u) ? lf_ex2(fmaf(__uint_as_float(v[k][e]), sl2, -m_ref)) : 0.f;
               const float p1 = (w[k] >> e & 2u) ? lf_ex2(fmaf(__uint_as_float(v[k][e + 1]), sl2, -m_ref)) : 0.f;
-              sum0 += p0;
-              sum1 += p1;
+              l += p0 + p1;
               pw[e / 2] = lf_pack2<kF16>(p0, p1);
             }
+            lf_tmem_st16(tP + 16 * k, pw);
           }
-          if (!waited) {  // the stream's last product has read P
-            ok = lf_pt_wait(bar + LF_PT_PV_DONE(g), (c - 1) & 1, abort_flag, P.status, 52);
-            if (!ok) break;
-            waited = true;
-            lf_tc_fence_after();
-          }
-          lf_tmem_st16(tP + 16 * k, pw);
         }
-        if (!ok) break;
-        l += sum0 + sum1;
         lf_tmem_wait_st();
       }
       lf_tc_fence_before();
