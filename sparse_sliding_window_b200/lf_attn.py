@@ -9,6 +9,7 @@ library cannot be loaded, every call raises.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Optional, Sequence
 
@@ -319,68 +320,42 @@ def lf_proj_set_timing_events(ev_start, ev_stop):
 
 # ------------------------------------- rotation, paged cache, paged decode --
 #
-# These calls check shapes, dtypes and devices here: the library sees bare
-# pointers, and a wrong shape would send a kernel out of its buffers.
+# These calls check shapes, dtypes and devices: the library sees bare
+# pointers, and a wrong shape would send a kernel out of its buffers.  The
+# checks are native (csrc/lf_bind.cpp): from Python they would take longer than
+# a decode step.
+
+BIND_PATH = os.path.join(HERE, "_lf_bind.so")
+_bind = None
+
+
+def _load_bind():
+    global _bind
+    if _bind is None:
+        load()
+        if not os.path.exists(BIND_PATH):
+            raise RuntimeError("_lf_bind.so is not built (python -m sparse_sliding_window_b200.build)")
+        import importlib.util
+        import torch  # noqa: F401  the module uses its libraries
+        spec = importlib.util.spec_from_file_location("_lf_bind", BIND_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _bind = module
+    return _bind
+
 
 def _bad(msg: str):
     raise LfError(LF_ERR_INVALID, msg)
 
 
-def _want(name: str, t, shape, dtype, dev: int, packed: bool = True):
-    """t is a tensor of this shape and dtype on CUDA device `dev`; packed:
-    contiguous, else only its last dimension."""
-    if t.shape == shape and t.dtype is dtype and t.get_device() == dev and (
-            t.is_contiguous() or not packed and t.stride(-1) == 1):
-        return t.data_ptr()
-    if t.shape != shape:
-        _bad("%s has shape %s, %s is wanted" % (name, tuple(t.shape), tuple(shape)))
-    if t.dtype is not dtype:
-        _bad("%s is %s, %s is wanted" % (name, t.dtype, dtype))
-    if t.get_device() != dev:
-        _bad("%s is on %s, the call on cuda:%d" % (name, t.device, dev))
-    _bad("%s is not contiguous%s" % (name, "" if packed else " in its last dimension"))
+def _done(result):
+    """None, an LF_* code of the library, or the text of a refused argument."""
+    if result is not None:
+        _bad(result) if isinstance(result, str) else _check(result)
 
 
-def _cuda_device(t, name: str) -> int:
-    if not t.is_cuda:
-        _bad("%s is not on a GPU" % name)
-    return t.get_device()
-
-
-def _launch(dev: int, stream, fn, *args):
-    """fn(*args, stream) with CUDA device `dev` current; stream None: its
-    current stream (its raw handle: building the Stream object costs 3 us, as
-    much as the launch)."""
-    import torch
-    if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(dev)
-    elif stream.device_index != dev:
-        _bad("the stream is on %s, the tensors on cuda:%d" % (stream.device, dev))
-    else:
-        handle = stream.cuda_stream
-    if torch._C._cuda_getDevice() == dev:
-        code = fn(*args, handle)
-    else:
-        with torch.cuda.device(dev):
-            code = fn(*args, handle)
-    if code:
-        _check(code)
-
-
-def _torch_dtype(code: int):
-    import torch
-    return (torch.float32, torch.bfloat16, torch.float16)[code]
-
-
-def _dtype_of(t, name: str) -> int:
-    import torch
-    code = {torch.float32: LF_F32, torch.bfloat16: LF_BF16, torch.float16: LF_F16}.get(t.dtype)
-    if code is None:
-        _bad("%s is %s: float32, bfloat16 or float16 is wanted" % (name, t.dtype))
-    return code
-
-
-_I64x2, _I64x6 = ctypes.c_int64 * 2, ctypes.c_int64 * 6
+def _on(stream):
+    return None if stream is None else (stream.device_index, stream.cuda_stream)
 
 
 def make_rope_params(rot_dim: int = 64, interleaved: bool = False, n_axes: int = 1,
@@ -389,6 +364,9 @@ def make_rope_params(rot_dim: int = 64, interleaved: bool = False, n_axes: int =
     """Build an lf_rope_params (the arrays are kept alive on it)."""
     r = lf_rope_params()
     r.rot_dim, r.interleaved, r.n_axes, r.base = rot_dim, int(interleaved), n_axes, float(base)
+    if freqs is None and 2 <= rot_dim <= 64 and rot_dim % 2 == 0 and 0 < base < math.inf:
+        # what the library would compute at every call
+        freqs = [math.pow(base, -2.0 * p / rot_dim) for p in range(rot_dim // 2)]
     for field, values, kind in (("pair_axis", pair_axis, ctypes.c_int32), ("freqs", freqs, ctypes.c_double)):
         if values is not None:
             if len(values) != (rot_dim or 64) // 2:
@@ -399,37 +377,15 @@ def make_rope_params(rot_dim: int = 64, interleaved: bool = False, n_axes: int =
     return r
 
 
-def _rope(fn, r, xs, outs, positions, stream):
-    if not 1 <= len(xs) <= 8 or len(outs) != len(xs):
-        _bad("1 to 8 tensors are wanted, and an output for each")
-    first = xs[0]
-    dev, code, dt = _cuda_device(first, "x"), _dtype_of(first, "x"), first.dtype
-    if first.dim() != 4:
-        _bad("x has %d dimensions, [B, heads, n, 64] is wanted" % first.dim())
-    B, _, n, _ = first.shape
-    tensors = []
-    for x, out in zip(xs, outs):
-        if x.dim() != 4:
-            _bad("x has %d dimensions, [B, heads, n, 64] is wanted" % x.dim())
-        heads = x.shape[1]
-        shape = (B, heads, n, 64)
-        tensors.append((_want("x", x, shape, dt, dev, False), _want("out", out, shape, dt, dev, False), heads,
-                        x.stride()[:3], out.stride()[:3]))
-    if positions is not None:
-        import torch
-        positions = _want("positions", positions, (r.n_axes, B, n), torch.int32, dev)
-    _launch(dev, stream, fn, ctypes.byref(r), B, n, code, len(xs), (lf_rope_tensor * len(xs))(*tensors), positions)
-
-
 def lf_rope_fwd(r, xs, outs, positions=None, stream=None):
-    """Rotate every x [B, heads, n, 64] of xs into its out (which may be x)
-    by positions int32 [n_axes, B, n] (None: the token index)."""
-    _rope(load().lf_rope_fwd, r, xs, outs, positions, stream)
+    """Rotate every x [B, heads, n, 64] of the list xs into its out (which may
+    be x) by positions int32 [n_axes, B, n] (None: the token index)."""
+    _done((_bind or _load_bind()).rope(False, r, xs, outs, positions, _on(stream)))
 
 
 def lf_rope_bwd(r, grads, outs, positions=None, stream=None):
     """The backward of lf_rope_fwd: gradients of its outputs -> of its inputs."""
-    _rope(load().lf_rope_bwd, r, grads, outs, positions, stream)
+    _done((_bind or _load_bind()).rope(True, r, grads, outs, positions, _on(stream)))
 
 
 def make_paged_params(B: int, H: int, Hkv: int, page_size: int, num_pages: int, max_pages: int, window: int = -1,
@@ -462,72 +418,21 @@ def paged_workspace(p, device="cuda"):
     return torch.zeros(nbytes, dtype=torch.uint8, device=device)  # status words start at zero
 
 
-def _paged(p, k_pages, v_pages, block_table, lengths, ws):
-    """The checks that append and decode share; returns (dtype, device, the
-    pointers of the pools, the table and the lengths)."""
-    import torch
-    dev, i32 = _cuda_device(k_pages, "k_pages"), torch.int32
-    code, B, hkv = p.dtype, p.B, p.Hkv
-    if not 0 <= code <= 2:
-        _bad("bad dtype %d" % code)
-    dt = _torch_dtype(code)
-    pool = (p.num_pages, hkv, p.page_size, 64)
-    ptrs = (_want("k_pages", k_pages, pool, dt, dev), _want("v_pages", v_pages, pool, dt, dev),
-            _want("block_table", block_table, (B, p.max_pages), i32, dev), _want("lengths", lengths, (B,), i32, dev))
-    if ws.dtype is not torch.uint8 or ws.get_device() != dev or not ws.is_contiguous():
-        _bad("the workspace is a contiguous uint8 tensor on cuda:%d" % dev)
-    return dt, dev, B, hkv, ptrs
-
-
 def lf_cache_append(p, rope, q, k, v, lengths, block_table, q_out, k_pages, v_pages, ws, cu_new=None,
                     positions=None, stream=None):
     """Append new tokens to the paged cache: q [T,H,64] (or None), k, v
     [T,Hkv,64], any strides (a projection's [1,H,T,64] is x[0].transpose(0, 1));
     K rotated by rope (None: not) and V go to the pages, rotated Q to q_out."""
-    import torch
-    dt, dev, B, hkv, (kp, vp, table, lens) = _paged(p, k_pages, v_pages, block_table, lengths, ws)
-    T = k.shape[0]
-    kv = (T, hkv, 64)
-    kq = _want("k", k, kv, dt, dev, False)
-    vq = _want("v", v, kv, dt, dev, False)
-    qp = qo = None
-    qs = ks = k.stride()
-    vs = v.stride()
-    if (q is None) != (q_out is None):
-        _bad("q and q_out go together")
-    if q is not None:
-        heads = (T, p.H, 64)
-        qp = _want("q", q, heads, dt, dev, False)
-        qo = _want("q_out", q_out, heads, dt, dev)
-        qs = q.stride()
-    if cu_new is not None:
-        cu_new = _want("cu_new", cu_new, (B + 1,), torch.int32, dev)
-    if positions is not None:
-        positions = _want("positions", positions, (1 if rope is None else rope.n_axes, T), torch.int32, dev)
-    _launch(dev, stream, load().lf_cache_append, ctypes.byref(p), None if rope is None else ctypes.byref(rope), T,
-            qp, kq, vq, _I64x6(qs[0], qs[1], ks[0], ks[1], vs[0], vs[1]), cu_new, lens, positions, table, qo, kp, vp,
-            ws.data_ptr(), ws.numel())
+    _done((_bind or _load_bind()).append(p, rope, q, k, v, lengths, block_table, q_out, k_pages, v_pages, ws, cu_new,
+                                         positions, _on(stream)))
 
 
 def lf_paged_decode(p, q, k_pages, v_pages, block_table, lengths, o, lse, ws, prefix_table=None, stream=None):
     """Decode step over the paged cache: q [B,H,64] (any strides) against the
     window of each sequence's own rows and the shared prefix; writes o
     [B,H,64] and lse [B,H] (or None)."""
-    import torch
-    dt, dev, B, _, (kp, vp, table, lens) = _paged(p, k_pages, v_pages, block_table, lengths, ws)
-    H = p.H
-    rows = (B, H, 64)
-    qp, op = _want("q", q, rows, dt, dev, False), _want("o", o, rows, dt, dev)
-    if lse is not None:
-        lse = _want("lse", lse, (B, H), torch.float32, dev)
-    prefix = p.prefix_len
-    if (prefix_table is None) != (prefix <= 0):
-        _bad("prefix_table goes with prefix_len > 0")
-    if prefix > 0:
-        prefix_table = _want("prefix_table", prefix_table, (-(-prefix // p.page_size),), torch.int32, dev)
-    _launch(dev, stream, load().lf_paged_decode, ctypes.byref(p), qp,
-            None if q.is_contiguous() else _I64x2(*q.stride()[:2]), kp, vp, table, lens, prefix_table, op, lse,
-            ws.data_ptr(), ws.numel())
+    _done((_bind or _load_bind()).decode(p, q, k_pages, v_pages, block_table, lengths, o, lse, ws, prefix_table,
+                                         _on(stream)))
 
 
 # ------------------------------------------------------------ convenience --
