@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(LF_PD_WARPS * 32)
   constexpr int BATCH = SUB * LF_PD_LOADS;
   __shared__ float s_m[LF_PD_WARPS][GT], s_l[LF_PD_WARPS][GT], s_acc[LF_PD_WARPS][GT][LF_HD];
   extern __shared__ float s_cl[];  // CTA 0 of a cluster: [cl][GT] m, l and [cl][GT][64]
-  const bool prefix = P.prefix_len > 0;
+  const bool prefix = P.nch > 0;  // parts of a prefix kernel to add
   // Behind a prefix kernel the call's inputs are already complete: every block
   // of that kernel waited for its own predecessors before it let this one start.
   if (!prefix) asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -63,8 +63,14 @@ __global__ void __launch_bounds__(LF_PD_WARPS * 32)
   const bool ok = lf_len_ok(len, P.max_pages, P.shift);
   if (!ok && threadIdx.x == 0 && crank == 0) lf_set_status(P.status, LF_ERR_DEVICE_INPUT, LF_DET_LENGTH + b);
   const int d = P.dil[hk];
-  const int nk = ok ? lf_window_keys(len, P.window, d) : 0;
+  const int own = ok ? lf_window_keys(len, P.window, d) : 0;
+  const int nk = own + (ok && P.direct ? P.prefix_len : 0);
   const int32_t *table = P.table + (size_t)b * P.max_pages;
+  const int pcols = (P.prefix_len + (1 << P.shift) - 1) >> P.shift;
+  auto row_of = [&](int k) {  // pool row of key k: the window, then the prefix
+    return k < own ? lf_pool_row(table, P.max_pages, P.num_pages, P.shift, P.Hkv, hk, len - 1 - k * d)
+                   : lf_pool_row(P.prefix_table, pcols, P.num_pages, P.shift, P.Hkv, hk, k - own);
+  };
 
   float qf[GT][N], acc[GT][N], m[GT], l[GT];
 #pragma unroll
@@ -86,9 +92,9 @@ __global__ void __launch_bounds__(LF_PD_WARPS * 32)
   // fetched while this one is worked on)
   int mine = LF_ROW_NONE;
   if (lane < BATCH && k0 + lane < nk)
-    mine = lf_pool_row(table, P.max_pages, P.num_pages, P.shift, P.Hkv, hk, len - 1 - (k0 + lane) * d);
+    mine = row_of(k0 + lane);
   for (; k0 < nk; k0 += step) {
-    if (mine == LF_ROW_BAD) lf_set_status(P.status, LF_ERR_DEVICE_INPUT, LF_DET_PAGE + b);
+    if (mine == LF_ROW_BAD) lf_set_status(P.status, LF_ERR_DEVICE_INPUT, k0 + lane < own ? LF_DET_PAGE + b : LF_DET_PREFIX);
     uint4 kr[LF_PD_LOADS], vr[LF_PD_LOADS];
     uint32_t have = 0;
 #pragma unroll
@@ -101,7 +107,7 @@ __global__ void __launch_bounds__(LF_PD_WARPS * 32)
     const int kn = k0 + step + lane;
     mine = LF_ROW_NONE;
     if (lane < BATCH && kn < nk)
-      mine = lf_pool_row(table, P.max_pages, P.num_pages, P.shift, P.Hkv, hk, len - 1 - kn * d);
+      mine = row_of(kn);
     float s[GT][LF_PD_LOADS];
 #pragma unroll
     for (int i = 0; i < LF_PD_LOADS; i++) {
@@ -242,12 +248,30 @@ __global__ void __launch_bounds__(LF_PD_WARPS * 32)
   }
 }
 
+// Keys of a sequence's own rows that a query can attend.
+static int64_t lf_most_keys(const LfPagedDev &P) {
+  const int64_t cap = (int64_t)P.max_pages << P.shift;
+  return P.window < 0 || P.window >= cap ? cap : P.window + 1;
+}
+
+// Few units (sequence, key/value head): the decode kernel reads the prefix for
+// every sequence itself, which saves a kernel and the merging of its parts.
+// With up to 37 units (8 CTAs each, two per SM) the repeated reads come from L2
+// and keep up to about here.  Measured, prefix kernel / direct, in us: f32 1 x 8
+// heads 1000 rows 8.4 / 5.7, 4000 rows 21.9 / 10.5; f32 36 x 1 heads 10.3 / 6.4
+// and 13.4 / 12.5; bf16 2 x 32/4 heads 2000 rows 12.3 / 7.5, 8000 rows 33.7 /
+// 11.1; bf16 36 x 1 heads 9.1 / 7.3 and 12.8 / 13.2; bf16 4 x 8 heads 6.3 / 7.4
+// and 14.1 / 13.2.
+bool lf_prefix_direct(const LfPagedDev &P, int dtype) {
+  const int64_t units = (int64_t)P.B * P.Hkv * ((P.G + 15) / 16);
+  return units * 8 <= 2 * 148 && P.prefix_len <= (dtype == LF_F32 ? 4096 : 8192);
+}
+
 // CTAs per unit (sequence, key/value head, query-head group): enough for four
 // per SM, at most as many as the longest possible window has steps of `step`
 // keys, and `most` (a power of two, up to 8, the portable cluster size).
 static int lf_pd_cluster(const LfPagedDev &P, int64_t units, int step, int most) {
-  const int64_t cap = (int64_t)P.max_pages << P.shift;
-  const int64_t keys = P.window < 0 || P.window >= cap ? cap : P.window + 1;
+  const int64_t keys = lf_most_keys(P) + (P.direct ? P.prefix_len : 0);
   const int64_t work = (keys + step - 1) / step;
   int cl = 1;
   while (cl < most && units * cl < 4 * lf_sm_count() && cl < work) cl *= 2;
@@ -406,7 +430,7 @@ __global__ void __launch_bounds__(128, 2)
   constexpr int RB = 16 * MT;
   extern __shared__ __align__(16) char smem_raw[];
   __shared__ float s_m[4][16], s_l[4][16];
-  const bool prefix = P.prefix_len > 0;
+  const bool prefix = P.nch > 0;  // parts of a prefix kernel to add
   // Behind a prefix kernel the call's inputs are already complete: every block
   // of that kernel waited for its own predecessors before it let this one start.
   if (!prefix) asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -420,12 +444,13 @@ __global__ void __launch_bounds__(128, 2)
   const bool ok = lf_len_ok(len, P.max_pages, P.shift);
   if (!ok && threadIdx.x == 0 && crank == 0) lf_set_status(P.status, LF_ERR_DEVICE_INPUT, LF_DET_LENGTH + b);
   const int d = P.dil[hk];
-  const int nk = ok ? lf_window_keys(len, P.window, d) : 0;
+  const int own = ok ? lf_window_keys(len, P.window, d) : 0;
+  const LfPmKeys keys{P.table + (size_t)b * P.max_pages, P.max_pages, own, len - 1, -d, LF_DET_PAGE + b,
+                      ok && P.direct ? P.prefix_len : 0};
   LfPmQ<MT> qa;
   lf_pd_queries<T, MT>(P, q, b, hk, g0, gn, qa);
   LfPmState<MT> S;
-  lf_pm_attend<T, MT>(P, LfPmKeys{P.table + (size_t)b * P.max_pages, P.max_pages, nk, len - 1, -d}, hk,
-                      LF_DET_PAGE + b, kp, vp, crank, cl, qa, (uint32_t)__cvta_generic_to_shared(smem_raw), S);
+  lf_pm_attend<T, MT>(P, keys, hk, kp, vp, crank, cl, qa, (uint32_t)__cvta_generic_to_shared(smem_raw), S);
 
   // Behind the warps' spilled states [4][16][64], shared memory of CTA 0 holds
   // the cluster's: acc [cl][gmax][64], m, l [cl][gmax].  The cluster barrier
@@ -572,7 +597,7 @@ __global__ void __launch_bounds__(128, MT == 1 ? 3 : 2)
   __shared__ float s_m[4][16], s_l[4][16];
   __shared__ int s_warp[4], s_last, s_at[2];
   __shared__ LfPdRun s_cut[2];
-  const bool prefix = P.prefix_len > 0;
+  const bool prefix = P.nch > 0;  // parts of a prefix kernel to add
   if (!prefix) asm volatile("griddepcontrol.wait;" ::: "memory");  // as in lf_paged_mma_kernel
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -669,14 +694,14 @@ __global__ void __launch_bounds__(128, MT == 1 ? 3 : 2)
     int fill = begin, slot = 0, st = 0;
     LfPmAhead A;
     auto lookup = [&]() {
-      lf_pm_lookup(P, LfPmKeys{P.table + (size_t)F.b * P.max_pages, P.max_pages, F.nk, F.len - 1, -F.d}, F.tile,
-                   fill < end, A);
+      lf_pm_lookup(P, LfPmKeys{P.table + (size_t)F.b * P.max_pages, P.max_pages, F.nk, F.len - 1, -F.d,
+                               LF_DET_PAGE + F.b, 0}, F.tile, fill < end, A);
     };
     lookup();
     auto load = [&]() {
       uint32_t h = 0;
       if (fill < end) {
-        h = lf_pm_load<T>(P, A, F.hk, LF_DET_PAGE + F.b, kp, vp, ring + slot * LF_PM_STAGE);
+        h = lf_pm_load<T>(P, A, F.hk, kp, vp, ring + slot * LF_PM_STAGE);
         lf_pd_next(P, s_len, ngroups, F);
         fill++;
         lookup();
@@ -790,11 +815,9 @@ void lf_paged_plan(LfPagedDev &P, int dtype) {
   P.run_ctas = 0;
   P.same_dil = 1;
   for (int h = 1; h < P.Hkv; h++) P.same_dil &= P.dil[h] == P.dil[0];
-  if (dtype == LF_F32 || P.B > LF_PDR_MAX_B) return;
+  if (dtype == LF_F32 || P.direct || P.B > LF_PDR_MAX_B) return;
   const int rb = lf_pdm_rows(P);
-  const int64_t units = (int64_t)P.B * P.Hkv * ((P.G + rb - 1) / rb);
-  const int64_t cap = (int64_t)P.max_pages << P.shift;
-  const int64_t keys = P.window < 0 || P.window >= cap ? cap : P.window + 1;
+  const int64_t units = (int64_t)P.B * P.Hkv * ((P.G + rb - 1) / rb), keys = lf_most_keys(P);
   const int64_t tiles = units * ((keys + LF_PM_KEYS - 1) / LF_PM_KEYS);
   if (units * 8 <= 2 * 148 || units > LF_PDR_MAX_UNITS || tiles >= 1ll << 31) return;
   const int per = 228 * 1024 / (lf_pdr_smem(P) + 1024 + 640);  // 1 KB of the system's, 640 static

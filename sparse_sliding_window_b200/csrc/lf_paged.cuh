@@ -49,11 +49,12 @@ struct LfRopeArgs {
   int32_t *status;
 };
 
-// nch: parts that the prefix kernel leaves per row; chunk: keys a block takes.
+// nch: parts that the prefix kernel leaves per row; chunk: keys a block takes;
+// direct: no prefix kernel (nch = 0), the decode kernel reads the prefix itself.
 struct LfPagedDev {
   int B, H, Hkv, G;      // G = H / Hkv
   int shift, num_pages, max_pages;
-  int window, prefix_len, nch, chunk;
+  int window, prefix_len, nch, chunk, direct;
   float scale_log2;
   int64_t qs[2];         // q strides: sequence, head
   const int32_t *table, *lengths, *prefix_table;
@@ -86,10 +87,11 @@ struct LfPagedLaunch {
 cudaError_t lf_launch_paged_decode(const LfPagedLaunch &L, const void *q, const void *kp,
                                    const void *vp, void *o, float *lse);
 cudaError_t lf_launch_prefix(const LfPagedLaunch &L, const void *q, const void *kp, const void *vp);
-// parts and keys per chunk of the prefix split
+// how the prefix is read: direct, or parts and keys per chunk of its split
 void lf_prefix_plan(LfPagedDev &d, int dtype);
 // the same of the tensor-core kernel (bf16, f16, more than 32 rows)
 cudaError_t lf_launch_prefix_tc(const LfPagedLaunch &L, const void *q, const void *kp, const void *vp);
 void lf_prefix_tc_plan(LfPagedDev &d);
+bool lf_prefix_direct(const LfPagedDev &d, int dtype);
 // run_ctas and same_dil
 void lf_paged_plan(LfPagedDev &d, int dtype);

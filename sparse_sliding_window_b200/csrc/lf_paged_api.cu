@@ -316,7 +316,7 @@ extern "C" int lf_paged_decode(const lf_paged_params *p, const void *q, const in
   L.dev.table = block_table;
   L.dev.lengths = lengths;
   L.dev.prefix_table = prefix_table;
-  if (p->prefix_len > 0 && (st = lp_cuda(lf_launch_prefix(L, q, k_pages, v_pages), "lf_paged_decode (prefix)")))
+  if (L.dev.nch > 0 && (st = lp_cuda(lf_launch_prefix(L, q, k_pages, v_pages), "lf_paged_decode (prefix)")))
     return st;
   return lp_cuda(lf_launch_paged_decode(L, q, k_pages, v_pages, o, lse), "lf_paged_decode");
 }

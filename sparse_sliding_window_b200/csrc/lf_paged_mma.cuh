@@ -79,39 +79,43 @@ template <int MT> struct LfPmState {
 };
 template <int MT> using LfPmQ = uint32_t[MT][4][4];  // A fragments: 16 rows x 64 channels each
 
-// Where the keys are: key k < nkeys is cache row first + k * step of the table.
+// Where the keys are: key k < nkeys is cache row first + k * step of the table
+// (detail: of the status when that has no page); the next nprefix keys are the
+// rows of the shared prefix.
 struct LfPmKeys {
   const int32_t *table;
-  int columns, nkeys, first, step;
+  int columns, nkeys, first, step, detail, nprefix;
 };
 
 // The page of key 32 warp + lane of a tile is fetched one tile early
 // (lf_pm_lookup) and only looked at when the tile is loaded (lf_pm_load): the
 // table's latency stays off the loop.
 struct LfPmAhead {
-  int page, row;
+  int page, row, detail;
 };
 __device__ __forceinline__ void lf_pm_lookup(const LfPagedDev &P, const LfPmKeys &K, int tile, bool take,
                                              LfPmAhead &A) {
   const int k = tile * LF_PM_KEYS + (int)threadIdx.x;
-  A.row = take && k < K.nkeys ? K.first + k * K.step : LF_ROW_NONE;
-  if (lf_row_ok(K.columns, P.shift, A.row))
-    A.page = K.table[A.row >> P.shift];
+  const bool own = k < K.nkeys;
+  A.row = !take || k >= K.nkeys + K.nprefix ? LF_ROW_NONE : own ? K.first + k * K.step : k - K.nkeys;
+  A.detail = own ? K.detail : LF_DET_PREFIX;
+  if (lf_row_ok(own ? K.columns : (P.prefix_len + (1 << P.shift) - 1) >> P.shift, P.shift, A.row))
+    A.page = (own ? K.table : P.prefix_table)[A.row >> P.shift];
   else
     A.row = LF_ROW_NONE;
 }
 
 // Starts the copies of the warp's 32 K and V rows into its stage `to` (eight
 // lanes a row: a copy instruction moves whole 128-byte rows); returns the mask
-// of the keys that count.  detail: of the status when a page is no page.
+// of the keys that count.
 template <typename T>
-__device__ __forceinline__ uint32_t lf_pm_load(const LfPagedDev &P, const LfPmAhead &A, int hk, int detail,
-                                               const T *kp, const T *vp, uint32_t to) {
+__device__ __forceinline__ uint32_t lf_pm_load(const LfPagedDev &P, const LfPmAhead &A, int hk, const T *kp,
+                                               const T *vp, uint32_t to) {
   const int lane = threadIdx.x % 32;
   int row = A.row;
   if (row >= 0) {
     row = lf_row_in_page(A.page, P.num_pages, P.shift, P.Hkv, hk, row);
-    if (row == LF_ROW_BAD) lf_set_status(P.status, LF_ERR_DEVICE_INPUT, detail);
+    if (row == LF_ROW_BAD) lf_set_status(P.status, LF_ERR_DEVICE_INPUT, A.detail);
   }
   const uint32_t have = __ballot_sync(0xffffffffu, row >= 0);
   if (have == 0) return 0;  // nothing will be read of the stage
@@ -248,10 +252,10 @@ template <int MT> __device__ __forceinline__ void lf_pm_sum(LfPmState<MT> &S) {
 // Tiles tile0, tile0 + tstep, ... of the keys; ring: the four warps' stages.
 // On return every copy of the warp has landed and been read.
 template <typename T, int MT>
-__device__ __forceinline__ void lf_pm_attend(const LfPagedDev &P, const LfPmKeys &K, int hk, int detail,
-                                             const T *kp, const T *vp, int tile0, int tstep,
-                                             const LfPmQ<MT> &qa, uint32_t ring, LfPmState<MT> &S) {
-  const int ntiles = (K.nkeys + LF_PM_KEYS - 1) / LF_PM_KEYS;
+__device__ __forceinline__ void lf_pm_attend(const LfPagedDev &P, const LfPmKeys &K, int hk, const T *kp,
+                                             const T *vp, int tile0, int tstep, const LfPmQ<MT> &qa,
+                                             uint32_t ring, LfPmState<MT> &S) {
+  const int ntiles = (K.nkeys + K.nprefix + LF_PM_KEYS - 1) / LF_PM_KEYS;
   ring += threadIdx.x / 32 * LF_PM_STAGES * LF_PM_STAGE;
   uint32_t ok[LF_PM_STAGES] = {};  // of the tiles in flight, oldest first
   int next = tile0, slot = 0, st = 0;
@@ -259,7 +263,7 @@ __device__ __forceinline__ void lf_pm_attend(const LfPagedDev &P, const LfPmKeys
   lf_pm_lookup(P, K, next, next < ntiles, A);
   auto load = [&]() {
     uint32_t have = 0;
-    if (next < ntiles) have = lf_pm_load<T>(P, A, hk, detail, kp, vp, ring + slot * LF_PM_STAGE);
+    if (next < ntiles) have = lf_pm_load<T>(P, A, hk, kp, vp, ring + slot * LF_PM_STAGE);
     lf_cp_commit();
     next += tstep;
     slot = slot + 1 == LF_PM_STAGES ? 0 : slot + 1;

@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(128, 2) lf_prefix_mma_kernel(const __grid_cons
     lf_pm_qfrag<T>(lf_px_row(P, q, hk, min(xa, rows - 1)), lf_px_row(P, q, hk, min(xa + 8, rows - 1)), qa[mt]);
   }
   LfPmState<MT> S;
-  lf_pm_attend<T, MT>(P, LfPmKeys{P.prefix_table, columns, nkeys, j0, 1}, hk, LF_DET_PREFIX, kp, vp, 0, 1, qa,
+  lf_pm_attend<T, MT>(P, LfPmKeys{P.prefix_table, columns, nkeys, j0, 1, LF_DET_PREFIX, 0}, hk, kp, vp, 0, 1, qa,
                       (uint32_t)__cvta_generic_to_shared(smem_raw), S);
   float *s_acc = reinterpret_cast<float *>(smem_raw);
 #pragma unroll
@@ -193,7 +193,8 @@ static int lf_prefix_rows(const LfPagedDev &d, int dtype) {
 void lf_prefix_plan(LfPagedDev &d, int dtype) {
   d.nch = 0;
   d.chunk = 0;
-  if (d.prefix_len <= 0) return;
+  d.direct = d.prefix_len > 0 && lf_prefix_direct(d, dtype);
+  if (d.prefix_len <= 0 || d.direct) return;
   if (lf_prefix_is_tc(d, dtype)) return lf_prefix_tc_plan(d);
   const int rb = lf_prefix_rows(d, dtype);
   const int64_t blocks = (int64_t)d.Hkv * ((d.B * d.G + rb - 1) / rb);

@@ -431,6 +431,11 @@ __global__ void __launch_bounds__(LF_PT_THREADS, 1) lf_prefix_tc_kernel(const __
           }
         }
         lf_tmem_wait_st();
+      } else if (c > 0) {
+        // A warp without rows must not arrive for this tile while the others
+        // still owe the last one: its arrival would complete their phase.
+        ok = lf_pt_wait(bar + LF_PT_PV_DONE(g), (c - 1) & 1, abort_flag, P.status, 54);
+        if (!ok) break;
       }
       lf_tc_fence_before();
       __syncwarp();

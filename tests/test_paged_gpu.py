@@ -139,6 +139,16 @@ PREFIX = [
     (4, 2, 16, [(b * 37) % 130 for b in range(60)] + [1500], -1, 90),
     (24, 1, 32, [b % 40 for b in range(80)], 10, 200),
     (48, 1, 16, [b % 20 for b in range(80)], -1, 33),
+    # few rows, but too many or too long for every sequence to read the prefix itself
+    (2, 2, 16, [b % 9 for b in range(20)], -1, 300),
+    (3, 3, 32, [b % 40 for b in range(13)], 12, 700),
+    (1, 1, 32, [5, 0, 90], -1, 9000),
+    (24, 2, 16, [7], 3, 8300),
+    # several tiles a block, with a row block that is full, half full, or has a few rows too many
+    (40, 40, 64, [b % 3 for b in range(40)], 4, 1500),
+    (38, 19, 16, [b % 5 for b in range(64)], 4, 1301),
+    (26, 26, 128, [b % 4 for b in range(97)], -1, 1152),
+    (12, 12, 64, [300 + b for b in range(64)], 64, 4096),
 ]
 
 
