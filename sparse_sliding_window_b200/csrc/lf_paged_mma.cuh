@@ -214,18 +214,22 @@ __device__ __forceinline__ void lf_pm_tile(const LfPmQ<MT> &qa, uint32_t sk, uin
       S.l[mt][1] += s[mt][n][2] + s[mt][n][3];
     }
   }
-  // P is rounded to the 16-bit type for the product with V (p <= 1, half a
-  // step relative each); the row sum keeps the unrounded values
+  // P enters the product with V as two 16-bit numbers, the rounded value and
+  // what the rounding left (p <= 1; together within a quarter of the square of
+  // a step), so that the output is rounded once, at its end: the loop waits for
+  // bytes, not for the second product.
 #pragma unroll
   for (int k = 0; k < 2; k++) {
-    uint32_t pa[MT][4];
+    uint32_t pa[MT][4], pb[MT][4];
 #pragma unroll
-    for (int mt = 0; mt < MT; mt++) {
-      pa[mt][0] = lf_pm_pack<T>(s[mt][2 * k][0], s[mt][2 * k][1]);
-      pa[mt][1] = lf_pm_pack<T>(s[mt][2 * k][2], s[mt][2 * k][3]);
-      pa[mt][2] = lf_pm_pack<T>(s[mt][2 * k + 1][0], s[mt][2 * k + 1][1]);
-      pa[mt][3] = lf_pm_pack<T>(s[mt][2 * k + 1][2], s[mt][2 * k + 1][3]);
-    }
+    for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const float p0 = s[mt][2 * k + i / 2][2 * (i % 2)], p1 = s[mt][2 * k + i / 2][2 * (i % 2) + 1];
+        pa[mt][i] = lf_pm_pack<T>(p0, p1);
+        const float2 r = LfIo<T>::ld2(reinterpret_cast<const T *>(&pa[mt][i]));
+        pb[mt][i] = lf_pm_pack<T>(p0 - r.x, p1 - r.y);
+      }
 #pragma unroll
     for (int n = 0; n < 8; n += 2) {
       uint32_t b[4];  // 16 keys x 16 channels, transposed
@@ -234,6 +238,8 @@ __device__ __forceinline__ void lf_pm_tile(const LfPmQ<MT> &qa, uint32_t sk, uin
       for (int mt = 0; mt < MT; mt++) {
         lf_mma16<T>(S.acc[mt][n], pa[mt], b[0], b[1]);
         lf_mma16<T>(S.acc[mt][n + 1], pa[mt], b[2], b[3]);
+        lf_mma16<T>(S.acc[mt][n], pb[mt], b[0], b[1]);
+        lf_mma16<T>(S.acc[mt][n + 1], pb[mt], b[2], b[3]);
       }
     }
   }
