@@ -129,13 +129,14 @@ __global__ void __launch_bounds__(LF_PD_WARPS * 32)
 #pragma unroll
       for (int i = 0; i < LF_PD_LOADS; i++) M = fmaxf(M, s[g][i]);
       const float f = lf_part_scale(m[g], M);
+      const float e = M == -INFINITY ? 0.f : M;  // no key yet, or scores of -inf alone: p = 0
       m[g] = M;
       l[g] *= f;
 #pragma unroll
       for (int j = 0; j < N; j++) acc[g][j] *= f;
 #pragma unroll
       for (int i = 0; i < LF_PD_LOADS; i++) {
-        s[g][i] = (have >> i & 1) ? lf_ex2(s[g][i] - M) : 0.f;
+        s[g][i] = (have >> i & 1) ? lf_ex2(s[g][i] - e) : 0.f;
         l[g] += s[g][i];
       }
     }

@@ -173,6 +173,8 @@ static int lp_prepare(const lf_paged_params *p, LfPagedLaunch &L) {
   if (!(p->scale >= 0.f) || isinf(p->scale)) return lp_fail(LF_ERR_INVALID, "scale must be finite and >= 0");
   if (p->prefix_len < 0 || p->prefix_len > 1 << 30)
     return lp_fail(LF_ERR_INVALID, "prefix_len must be 0..2^30 (got %d)", p->prefix_len);
+  if (p->prefix_len > 0 && (long long)p->B * (p->H / p->Hkv) > 2000000)
+    return lp_fail(LF_ERR_UNSUPPORTED, "more than 2000000 queries per key/value head behind a prefix");
   LfPagedDev &d = L.dev;
   memset(&d, 0, sizeof(d));
   for (int h = 0; h < p->Hkv; h++) {

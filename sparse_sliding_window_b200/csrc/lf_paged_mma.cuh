@@ -215,9 +215,10 @@ __device__ __forceinline__ void lf_pm_tile(const LfPmQ<MT> &qa, uint32_t sk, uin
     }
   }
   // P enters the product with V as two 16-bit numbers, the rounded value and
-  // what the rounding left (p <= 1; together within a quarter of the square of
-  // a step), so that the output is rounded once, at its end: the loop waits for
-  // bytes, not for the second product.
+  // what the rounding left (p <= 1; together within the square of half a step),
+  // so that the output is rounded once, at its end: with one number alone the
+  // error against 64 bits is 1.4 times that of the output's own rounding.  The
+  // second product costs 1 to 5% of a decode step.
 #pragma unroll
   for (int k = 0; k < 2; k++) {
     uint32_t pa[MT][4], pb[MT][4];

@@ -96,13 +96,13 @@ __global__ void __launch_bounds__(256) lf_prefix_simt_kernel(const __grid_consta
         if (ok[i]) M = fmaxf(M, s[u][i]);
 #pragma unroll
       for (int w = 8; w > 0; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
-      const float f = m[u] == -INFINITY ? 0.f : lf_ex2(m[u] - M);
+      const float f = lf_part_scale(m[u], M), e = M == -INFINITY ? 0.f : M;
       m[u] = M;
       l[u] *= f;
 #pragma unroll
       for (int i = 0; i < 4; i++) {
         acc[u][i] *= f;
-        const float p = ok[i] ? lf_ex2(s[u][i] - M) : 0.f;
+        const float p = ok[i] ? lf_ex2(s[u][i] - e) : 0.f;
         l[u] += p;
         S.p[r + 16 * u][c + 16 * i] = p;
       }

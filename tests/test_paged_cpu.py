@@ -138,7 +138,7 @@ def test_workspace_sizes(lib):
     for bad in (dict(B=0), dict(H=0), dict(Hkv=0), dict(Hkv=3), dict(H=256, Hkv=2), dict(page_size=8), dict(page_size=24),
                 dict(page_size=2048), dict(num_pages=0), dict(max_pages=0), dict(dtype=3), dict(prefix_len=-1),
                 dict(prefix_len=2 ** 30 + 1), dict(head_dim=128), dict(scale=-1.0), dict(scale=float("nan")),
-                dict(scale=float("inf")), dict(dilation=[1, 0]), dict(window=-1, dilation=[1, 2]), dict(B=1000000),
+                dict(scale=float("inf")), dict(dilation=[1, 0]), dict(window=-1, dilation=[1, 2]), dict(B=1000000), dict(B=999999, H=6, prefix_len=10),
                 dict(num_pages=2 ** 27), dict(max_pages=2 ** 26 + 1)):
         assert L.lf_paged_workspace_size(L.make_paged_params(**{**GOOD, **bad})) == 0, bad
         assert lib.lf_attn_last_error(), bad

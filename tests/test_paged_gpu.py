@@ -240,6 +240,68 @@ def test_decode_leaves_out_bad_pages_and_lengths(dtype, prefix):
         R.check("o", R.f64(got), ro, to + 2.0 ** -22 + R.half_step(dtype) * (np.abs(ro) + to))
 
 
+@pytest.mark.parametrize("dtype", R.DTYPES)
+@pytest.mark.parametrize("B,Hkv,prefix", [(2, 1, 0), (2, 1, 200), (40, 2, 200), (80, 1, 0)])
+def test_decode_scores_of_minus_infinity_weigh_nothing(dtype, B, Hkv, prefix):
+    """Keys whose score is -inf (the newest ones, whole batches and tiles of
+    them) have probability 0: the rest is the softmax over the other keys."""
+    import torch
+    gone, n = 150, 260
+    c = Cache(77, dtype, B, Hkv, 16, [n] * B, prefix)
+    q = _normal(c.rng, (B, 2 * Hkv, 64), dtype)
+    q[..., 0] = q[..., 0].abs() + 0.5
+    for b in range(B):
+        for j in range(n - gone, n):
+            c.k[c.table[b, j // 16], :, j % 16, 0] = -math.inf
+    for j in range(0, prefix, 2):
+        c.k[c.prefix_table[j // 16], :, j % 16, 0] = -math.inf
+    p = c.params(2 * Hkv)
+    ws = L.paged_workspace(p)
+    o, lse = torch.empty_like(q), torch.empty(B, 2 * Hkv, device="cuda")
+    L.lf_paged_decode(p, q, c.k, c.v, c.t_table, c.t_lengths, o, lse, ws, prefix_table=c.t_prefix)
+    L.lf_attn_status(ws)
+    k, v, qq = R.f64(c.k), R.f64(c.v), R.f64(q)
+    for b in (0, B - 1):
+        for h in range(2 * Hkv):
+            kk, vv = (np.concatenate([R.cache_rows(x, c.prefix_table, prefix, h // 2)[1::2],
+                                      R.cache_rows(x, c.table[b], n, h // 2)[:n - gone]]) for x in (k, v))
+            ro, rl, to, tl = R.softmax_row(qq[b, h], kk, vv, 0.125, R.half_step(dtype))
+            R.check("o", R.f64(o[b, h]), ro, to + 2.0 ** -22 + R.half_step(dtype) * (np.abs(ro) + to))
+            R.check("lse", R.f64(lse[b, h]), rl, tl)
+
+
+@pytest.mark.parametrize("B,prefix", [(2, 0), (40, 0), (40, 150), (1, 9000)])
+def test_pools_beyond_2_31_elements(B, prefix):
+    """Pages at the end of pools of more than 2^31 elements: append, then decode
+    by each of the kernels, against the same rows in a small pool."""
+    import torch
+    page, cols, num = 1024, 2, 2 ** 21 // 64 + 2 * 40 + 20
+    small = B * cols + 12
+    far = num - small                       # the big pool's last pages are the small pool's
+    big = [torch.empty(num, 1, page, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    assert big[0].numel() > 2 ** 31 and far * page * 64 > 2 ** 31 - 2 ** 23
+    rng = np.random.default_rng(13)
+    pools = [_normal(rng, (small, 1, page, 64), "bf16") for _ in range(2)]
+    for x, y in zip(big, pools):
+        x[far:] = y
+    table = torch.from_numpy(rng.permutation(small)[:B * cols].reshape(B, cols).astype(np.int32)).cuda()
+    pre = torch.arange(small - 9, small, dtype=torch.int32, device="cuda")[:-(-prefix // page)] if prefix else None
+    lengths = torch.full((B,), 1500, dtype=torch.int32, device="cuda")
+    q, k, v = (_normal(rng, (B, h, 64), "bf16") for h in (2, 1, 1))
+    out = []
+    for n, (kp, vp), off in ((small, pools, 0), (num, big, far)):
+        p = L.make_paged_params(B, 2, 1, page, n, cols, 300, None, 0.0, L.LF_BF16, prefix)
+        ws = L.paged_workspace(p)
+        qo, o, lse = torch.empty_like(q), torch.empty_like(q), torch.empty(B, 2, device="cuda")
+        t = table + off
+        L.lf_cache_append(p, L.make_rope_params(), q, k, v, lengths, t, qo, kp, vp, ws)
+        L.lf_paged_decode(p, qo, kp, vp, t, lengths, o, lse, ws, prefix_table=None if pre is None else pre + off)
+        L.lf_attn_status(ws)
+        out.append((o, lse))
+    assert torch.equal(out[0][0], out[1][0]) and torch.equal(out[0][1], out[1][1])
+    assert all(torch.equal(x[far:], y) for x, y in zip(big, pools))     # the appended rows, and no other
+
+
 def test_decode_captured_and_two_graphs_share_a_workspace():
     """Replays follow the lengths and tables of the moment; two graphs with one
     workspace, replayed one after the other, do not disturb each other."""
