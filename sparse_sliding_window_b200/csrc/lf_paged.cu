@@ -442,14 +442,14 @@ __global__ void __launch_bounds__(128, 2)
   const int gc = unit % ngroups, hk = unit / ngroups % P.Hkv, b = unit / ngroups / P.Hkv;
   const int g0 = gc * RB, gn = min(RB, P.G - g0);  // query heads of this unit
   const int len = P.lengths[b];
+  LfPmQ<MT> qa;  // on their way with the length
+  lf_pd_queries<T, MT>(P, q, b, hk, g0, gn, qa);
   const bool ok = lf_len_ok(len, P.max_pages, P.shift);
   if (!ok && threadIdx.x == 0 && crank == 0) lf_set_status(P.status, LF_ERR_DEVICE_INPUT, LF_DET_LENGTH + b);
   const int d = P.dil[hk];
   const int own = ok ? lf_window_keys(len, P.window, d) : 0;
   const LfPmKeys keys{P.table + (size_t)b * P.max_pages, P.max_pages, own, len - 1, -d, LF_DET_PAGE + b,
                       ok && P.direct ? P.prefix_len : 0};
-  LfPmQ<MT> qa;
-  lf_pd_queries<T, MT>(P, q, b, hk, g0, gn, qa);
   LfPmState<MT> S;
   lf_pm_attend<T, MT>(P, keys, hk, kp, vp, crank, cl, qa, (uint32_t)__cvta_generic_to_shared(smem_raw), S);
 
