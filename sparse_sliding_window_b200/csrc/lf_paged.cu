@@ -649,7 +649,7 @@ __global__ void __launch_bounds__(128, MT == 1 ? 3 : 2)
   // the nearer of its ends (handing the parts of a unit over costs as much as
   // some tiles).  Lanes 0 and 1 of warp 0 find the two cuts' units.
   LfPdCuts cuts;
-  cuts.n = min((int)gridDim.x, max(1, total / LF_PDR_LEAST));
+  cuts.n = min((int)gridDim.x, max(1, total));
   cuts.per = total / cuts.n;
   cuts.more = total - cuts.per * cuts.n;
   const int me = blockIdx.x;
@@ -820,7 +820,13 @@ void lf_paged_plan(LfPagedDev &P, int dtype) {
   const int rb = lf_pdm_rows(P);
   const int64_t units = (int64_t)P.B * P.Hkv * ((P.G + rb - 1) / rb), keys = lf_most_keys(P);
   const int64_t tiles = units * ((keys + LF_PM_KEYS - 1) / LF_PM_KEYS);
-  if (units * 8 <= 2 * 148 || units > LF_PDR_MAX_UNITS || tiles >= 1ll << 31) return;
+  // Few units stay with a cluster each: its CTAs fit the GPU at once and need
+  // no list.  Measured, clusters / runs, bf16, in us: 16 units of 8 heads with a
+  // window of 257 keys 4.3 / 6.5, 64 units 5.5 / 6.6, 144 units 9.7 / 8.1; every
+  // row up to 4000: 32 units 9.0 / 11.0, 64 units 16.4 / 15.5, 128 units 29.0 /
+  // 25.1; up to 16000: 16 units 19.4 / 25.6, 64 units 36.6 / 34.6.
+  const int few = P.nch == 0 && keys <= 512 ? 4 * 148 : 2 * 148;
+  if (units * 8 <= few || units > LF_PDR_MAX_UNITS || tiles >= 1ll << 31) return;
   const int per = 228 * 1024 / (lf_pdr_smem(P) + 1024 + 640);  // 1 KB of the system's, 640 static
   const int most = rb == 16 ? 3 : 2;
   const int64_t ctas = 148 * (per < most ? per : most);
