@@ -114,6 +114,14 @@ DECODE = [
     (40, 1, 64, [b % 70 for b in range(80)], 30, None),
     (96, 1, 16, [b % 40 for b in range(41)], -1, None),
     (1, 1, 16, [b % 19 for b in range(1100)], -1, None),
+    # units on both sides of the choice between the kernels, short and long windows
+    (5, 5, 16, [(b * 97) % 600 for b in range(14)], 511, [1, 2, 3, 1, 1]),
+    (10, 5, 16, [(b * 97) % 600 for b in range(15)], 511, [1, 2, 3, 1, 1]),
+    (5, 5, 16, [(b * 97) % 600 for b in range(14)], 512, [1, 2, 3, 1, 1]),
+    (16, 4, 64, [(b * 41) % 300 for b in range(18)], 256, None),
+    (37, 37, 32, [700, 513], 40, None),
+    (37, 37, 32, [700], -1, None),
+    (38, 38, 32, [700], -1, None),
 ]
 
 
@@ -270,7 +278,7 @@ def test_decode_scores_of_minus_infinity_weigh_nothing(dtype, B, Hkv, prefix):
             R.check("lse", R.f64(lse[b, h]), rl, tl)
 
 
-@pytest.mark.parametrize("B,prefix", [(2, 0), (40, 0), (40, 150), (1, 9000)])
+@pytest.mark.parametrize("B,prefix", [(2, 0), (40, 0), (80, 0), (40, 150), (1, 9000)])
 def test_pools_beyond_2_31_elements(B, prefix):
     """Pages at the end of pools of more than 2^31 elements: append, then decode
     by each of the kernels, against the same rows in a small pool."""
