@@ -19,7 +19,8 @@
  * of the workspace (lf_attn_status).  Tensors of one call share a dtype
  * (LF_F32, LF_BF16, LF_F16) and are 16-byte aligned; int32 arrays are 4-byte
  * aligned.  Strides count elements; the last dimension (64 channels) is
- * contiguous and every other stride is a multiple of 16 bytes.
+ * contiguous and every other stride is a multiple of 16 bytes.  An output
+ * overlaps no other tensor of its call, except where it is said that it may.
  */
 #ifndef LF_PAGED_H
 #define LF_PAGED_H
