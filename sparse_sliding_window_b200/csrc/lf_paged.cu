@@ -20,7 +20,7 @@ namespace cg = cooperative_groups;
 // state: o = a / L, lse = log of the sum, 0 and -inf where nothing was attended.
 template <typename T>
 __device__ __forceinline__ void lf_pd_write(T *o, float *lse, size_t row, int c, float M, float L, float a) {
-  const bool none = M == -INFINITY;
+  const bool none = M == -INFINITY && L == 0.f;  // (a NaN query has L = NaN)
   LfIo1<T>::st(o + row * LF_HD + c, none ? 0.f : a / L);
   if (lse && c == 0) lse[row] = none ? -INFINITY : (M + log2f(L)) * LF_LN2;
 }
@@ -166,9 +166,8 @@ __global__ void __launch_bounds__(LF_PD_WARPS * 32)
 #pragma unroll
           for (int j = 0; j < N; j += 4)
             *reinterpret_cast<float4 *>(a + j) = __ldcg(reinterpret_cast<const float4 *>(P.part_acc + at * LF_HD + lr * N + j));
-          if (ml.x == -INFINITY) continue;
           const float M = fmaxf(m[g], ml.x);
-          const float f = lf_part_scale(m[g], M), e = lf_ex2(ml.x - M);
+          const float f = lf_part_scale(m[g], M), e = lf_part_scale(ml.x, M);
           m[g] = M;
           l[g] = l[g] * f + ml.y * e;
 #pragma unroll

@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(LF_PT_THREADS, 1) lf_prefix_tc_kernel(const __
     const float sl2 = P.scale_log2;
     const LfPair sl2p = lf_pair(sl2, sl2);
     float m_ref = 0.f, l = 0.f;
-    bool fresh = true, ok = true;  // fresh: no key has counted yet
+    bool fresh = true, ok = true;  // fresh: no score above -inf yet
     int c = 0;                     // the stream's tile
     for (int i = g; i < n; i += LF_PT_G, c++) {
       const int s = i % LF_PT_NS;
@@ -376,12 +376,13 @@ __global__ void __launch_bounds__(LF_PT_THREADS, 1) lf_prefix_tc_kernel(const __
           if (!ok) break;
           lf_tc_fence_after();
         }
-        if (fresh && (w[0] | w[1]) != 0u) {
+        if (fresh && mt > -INFINITY) {
           // O holds nothing yet (or products of zeros): the reference moves freely
-          m_ref = mt == -INFINITY ? 0.f : mt;
+          m_ref = mt;
           fresh = false;
-        } else if (__any_sync(0xffffffffu, mt > m_ref + LF_PT_LAG)) {
-          const bool up = mt > m_ref + LF_PT_LAG;
+        }
+        if (__any_sync(0xffffffffu, !fresh && mt > m_ref + LF_PT_LAG)) {
+          const bool up = !fresh && mt > m_ref + LF_PT_LAG;
           const float f = up ? lf_ex2(m_ref - mt) : 1.f;
           if (up) m_ref = mt;
           l *= f;
@@ -446,7 +447,7 @@ __global__ void __launch_bounds__(LF_PT_THREADS, 1) lf_prefix_tc_kernel(const __
     if (ok && c > 0) ok = lf_pt_wait(bar + LF_PT_PV_DONE(g), (c - 1) & 1, abort_flag, P.status, 52);
     lf_tmem_wait_st();  // (an abort may leave stores in flight)
     float2 *s_ml = reinterpret_cast<float2 *>(misc + LF_PT_ML);
-    s_ml[g * 128 + row] = make_float2(fresh ? -INFINITY : m_ref, l);
+    s_ml[g * 128 + row] = make_float2(fresh ? -INFINITY : m_ref, l);  // (l of NaN scores stays)
     lf_tc_fence_before();
     asm volatile("bar.sync 1, %0;" ::"n"(LF_PT_SOFT) : "memory");  // every softmax warp comes here
     lf_tc_fence_after();

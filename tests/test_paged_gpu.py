@@ -278,6 +278,69 @@ def test_decode_scores_of_minus_infinity_weigh_nothing(dtype, B, Hkv, prefix):
             R.check("lse", R.f64(lse[b, h]), rl, tl)
 
 
+@pytest.mark.parametrize("dtype", R.DTYPES)
+@pytest.mark.parametrize("B,Hkv,prefix", [(2, 1, 200), (40, 2, 0), (20, 2, 900), (40, 2, 200), (70, 20, 1500)])
+def test_decode_low_scores_beside_scores_of_minus_infinity(dtype, B, Hkv, prefix):
+    """Whole tiles of scores of -inf, before and between scores of about -300
+    (exp of which is 0 in float32): the softmax over the latter."""
+    import torch
+    n = 400
+    c = Cache(78, dtype, B, Hkv, 16, [n] * B, prefix)
+    q = _normal(c.rng, (B, 2 * Hkv, 64), dtype)
+    q[..., 0] = q[..., 0].abs() + 0.5
+    q[..., 1] = 4
+    gone = [j for j in range(n) if (n - 1 - j) // 128 % 2 == 0]
+    pgone = [j for j in range(prefix) if j // 64 % 2 == 0]
+    c.k[..., 1] = -600
+    for b in range(B):
+        for j in gone:
+            c.k[c.table[b, j // 16], :, j % 16, 0] = -math.inf
+    for j in pgone:
+        c.k[c.prefix_table[j // 16], :, j % 16, 0] = -math.inf
+    p = c.params(2 * Hkv)
+    ws = L.paged_workspace(p)
+    o, lse = torch.empty_like(q), torch.empty(B, 2 * Hkv, device="cuda")
+    L.lf_paged_decode(p, q, c.k, c.v, c.t_table, c.t_lengths, o, lse, ws, prefix_table=c.t_prefix)
+    L.lf_attn_status(ws)
+    k, v, qq = R.f64(c.k), R.f64(c.v), R.f64(q)
+    rows, prows = np.setdiff1d(np.arange(n), gone), np.setdiff1d(np.arange(prefix), pgone)
+    for b in (0, B - 1):
+        for h in range(2 * Hkv):
+            kk, vv = (np.concatenate([R.cache_rows(x, c.prefix_table, prefix, h // 2)[prows],
+                                      R.cache_rows(x, c.table[b], n, h // 2)[rows]]) for x in (k, v))
+            ro, rl, to, tl = R.softmax_row(qq[b, h], kk, vv, 0.125, R.half_step(dtype))
+            R.check("o", R.f64(o[b, h]), ro, to + 2.0 ** -22 + R.half_step(dtype) * (np.abs(ro) + to))
+            R.check("lse", R.f64(lse[b, h]), rl, tl)
+
+
+@pytest.mark.parametrize("dtype", R.DTYPES)
+@pytest.mark.parametrize("B,Hkv,prefix", [(3, 1, 0), (3, 1, 150), (20, 2, 900), (40, 2, 200), (80, 1, 0), (80, 1, 40)])
+def test_decode_nan_query_stays_nan_and_its_own(dtype, B, Hkv, prefix):
+    """A NaN in a query makes its output and lse NaN; the other queries' bits
+    stay, and so does the zero of a query without keys."""
+    import torch
+    c = Cache(79, dtype, B, Hkv, 16, [0] + [200] * (B - 1), prefix)
+    q = _normal(c.rng, (B, 4 * Hkv, 64), dtype)
+    p = c.params(4 * Hkv)
+    ws = L.paged_workspace(p)
+    out = []
+    for bad in (False, True):
+        if bad:
+            q[1, 2, 5] = math.nan
+        o, lse = torch.empty_like(q), torch.empty(B, 4 * Hkv, device="cuda")
+        L.lf_paged_decode(p, q, c.k, c.v, c.t_table, c.t_lengths, o, lse, ws, prefix_table=c.t_prefix)
+        L.lf_attn_status(ws)
+        out.append((o, lse))
+    assert out[1][0][1, 2].isnan().all() and out[1][1][1, 2].isnan()
+    for x, y in zip(out[0], out[1]):
+        assert not x.isnan().any()
+        y = y.clone()
+        y[1, 2] = x[1, 2]
+        assert torch.equal(x, y)
+    if not prefix:
+        assert (out[0][0][0] == 0).all() and (out[0][1][0] == -math.inf).all()
+
+
 @pytest.mark.parametrize("B,prefix", [(2, 0), (40, 0), (80, 0), (40, 150), (1, 9000)])
 def test_pools_beyond_2_31_elements(B, prefix):
     """Pages at the end of pools of more than 2^31 elements: append, then decode
