@@ -7,8 +7,9 @@
 //   warps 0-11  softmax of streams 0, 1, 2 (four each)
 //   warp 12     loads K and V tiles by TMA, a box per page, into a ring
 //   warps 13-15 issue S = Q K^T (128 x 64 x 64) and O += P V (128 x 64 x 64) of
-//               their stream (one warp for all three needs about 780 cycles a
-//               tile for its waits and issues, more than the softmax)
+//               their stream, P as two 16-bit numbers (one warp for all three
+//               needs about 780 cycles a tile for its waits and issues, more than
+//               the softmax)
 // What bounds it is the softmax: 128 x 64 exponentials a tile at 16 a cycle
 // and SM, and, around them, a chain of barrier and TMEM waits of about 1200
 // cycles per step of a stream.  S is read into registers whole and handed back
@@ -28,13 +29,14 @@
 #define LF_PT_G 3        // streams
 #define LF_PT_SOFT (128 * LF_PT_G)
 #define LF_PT_THREADS (LF_PT_SOFT + 32 * (1 + LF_PT_G))
-#define LF_PT_NS 12      // K/V tiles in the ring (16 KB each)
+#define LF_PT_NS 9       // K/V tiles in the ring (16 KB each; with 8 of them 0.5 of 43 us slower, with 10 the same)
 #define LF_PT_TILE (LF_PT_KEYS * 128)
 
 #define LF_PT_Q 0
 #define LF_PT_K(s) (16384 + (s)*2 * LF_PT_TILE)
 #define LF_PT_V(s) (LF_PT_K(s) + LF_PT_TILE)
-#define LF_PT_MISC LF_PT_K(LF_PT_NS)
+#define LF_PT_L(g) (LF_PT_K(LF_PT_NS) + (g)*LF_PT_ROWS * 128)  // P's second numbers, per stream, laid out like Q
+#define LF_PT_MISC LF_PT_L(LF_PT_G)
 // barriers, from LF_PT_MISC
 #define LF_PT_KV_FULL(s) (8 * (s))
 #define LF_PT_KV_EMPTY(s) (8 * (LF_PT_NS + (s)))
@@ -99,36 +101,28 @@ __device__ __forceinline__ void lf_pt_drain(uint32_t bar, uint32_t parity, int32
   }
 }
 
-// ---- pairs of float32 in one 64-bit register (sm_100 packed arithmetic)
-typedef unsigned long long LfPair;
-__device__ __forceinline__ LfPair lf_pair(float a, float b) {
-  LfPair r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ LfPair lf_pair_u(uint32_t a, uint32_t b) {
-  LfPair r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ void lf_unpair(LfPair p, float &a, float &b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
-}
-__device__ __forceinline__ LfPair lf_fma2(LfPair a, LfPair b, LfPair c) {
-  LfPair r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ LfPair lf_add2(LfPair a, LfPair b) {
-  LfPair r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 __device__ __forceinline__ float lf_max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+// D (+)= A B with A (128 x 64, laid out like Q) and B (64 keys of V) in shared
+// memory: four K = 16 steps, no commit; acc = 0: the first step overwrites D.
+__device__ __forceinline__ void lf_pt_mma_low(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred e, pa;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+      "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\t"
+      "add.s64 b1, %2, 128;\n\tadd.s64 b2, %2, 256;\n\tadd.s64 b3, %2, 384;\n\t"
+      "setp.ne.b32 pa, %4, 0;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, pa;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, 1;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, 1;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, 1;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
 struct LfPtParams {
   CUtensorMap k, v;  // the pools as rows of 64, boxes of box_rows rows
   LfPagedDev dev;
@@ -280,6 +274,7 @@ __global__ void __launch_bounds__(LF_PT_THREADS, 1) lf_prefix_tc_kernel(const __
       const uint32_t id_s = lf_idesc(kF16, LF_PT_KEYS, 0), id_pv = lf_idesc(kF16, LF_HD, 1);
       const uint64_t slot = 2 * LF_PT_TILE >> 4;
       const int g = warp - LF_PT_SOFT / 32 - 1;
+      const uint64_t dl = lf_sdesc(sbase + LF_PT_L(g), 16, 1024);
       auto issue_s = [&](int i) {
         const int s = i % LF_PT_NS;
         if (!lf_pt_wait(bar + LF_PT_KV_FULL(s), (i / LF_PT_NS) & 1, abort_flag, P.status, 44)) return false;
@@ -301,8 +296,9 @@ __global__ void __launch_bounds__(LF_PT_THREADS, 1) lf_prefix_tc_kernel(const __
         ok = lf_pt_wait(bar + LF_PT_P_FULL(g), c & 1, abort_flag, P.status, 47);
         if (!ok) break;
         lf_tc_fence_after();
+        lf_pt_mma_low(tmem + LF_PT_TO(g), dl, dv + s * slot, id_pv, c > 0 ? 1u : 0u);
         lf_mma_ts_phase(tmem + LF_PT_TO(g), tmem + LF_PT_TP(g), dv + s * slot, 2048 >> 4, id_pv,
-                        (1u << (LF_PT_KEYS / 16)) - 1u, c > 0 ? 1u : 0u, bar + LF_PT_KV_EMPTY(s),
+                        (1u << (LF_PT_KEYS / 16)) - 1u, 1u, bar + LF_PT_KV_EMPTY(s),
                         bar + LF_PT_PV_DONE(g), 0u);
       }
       // every MMA of the three warps has completed once the barrier flips (TMEM is
@@ -395,14 +391,17 @@ __global__ void __launch_bounds__(LF_PT_THREADS, 1) lf_prefix_tc_kernel(const __
             lf_tmem_st16(tO + e, ov);
           }
         }
-        // P is rounded to the 16-bit type for the product with V (p < 2^8,
-        // half a step relative each); the row sum keeps the unrounded values
+        // P enters the product with V as two 16-bit numbers: the first through
+        // TMEM, the second, for which TMEM has no room, through shared memory.
+        // (One number alone: 128 x 16/4 heads on 16384 rows 38.4 us instead of
+        // 43.0, 64 x 12 heads on 4096 rows 25.8 instead of 27.3.)
+        uint8_t *low = lf_smem_raw + LF_PT_L(g) + row * 128;
         if (all) {
           LfPair sums[2] = {lf_pair(0.f, 0.f), lf_pair(0.f, 0.f)};
           const LfPair refp = lf_pair(-m_ref, -m_ref);
 #pragma unroll
           for (int k = 0; k < 2; k++) {
-            uint32_t pw[16];
+            uint32_t pw[16], pl[4];
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
               float p0, p1;
@@ -410,7 +409,9 @@ __global__ void __launch_bounds__(LF_PT_THREADS, 1) lf_prefix_tc_kernel(const __
               p0 = lf_ex2(p0);
               p1 = lf_ex2(p1);
               sums[e / 2 % 2] = lf_add2(sums[e / 2 % 2], lf_pair(p0, p1));
-              pw[e / 2] = lf_pack2<kF16>(p0, p1);
+              lf_p_split<kF16>(p0, p1, pw[e / 2], pl[e / 2 % 4]);
+              if (e % 8 == 6)
+                *reinterpret_cast<uint4 *>(low + (((4 * k + e / 8) ^ (row & 7)) << 4)) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
             }
             lf_tmem_st16(tP + 16 * k, pw);
           }
@@ -420,18 +421,21 @@ __global__ void __launch_bounds__(LF_PT_THREADS, 1) lf_prefix_tc_kernel(const __
         } else {
 #pragma unroll
           for (int k = 0; k < 2; k++) {
-            uint32_t pw[16];
+            uint32_t pw[16], pl[4];
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
               const float p0 = (w[k] >> e & 1u) ? lf_ex2(fmaf(__uint_as_float(v[k][e]), sl2, -m_ref)) : 0.f;
               const float p1 = (w[k] >> e & 2u) ? lf_ex2(fmaf(__uint_as_float(v[k][e + 1]), sl2, -m_ref)) : 0.f;
               l += p0 + p1;
-              pw[e / 2] = lf_pack2<kF16>(p0, p1);
+              lf_p_split<kF16>(p0, p1, pw[e / 2], pl[e / 2 % 4]);
+              if (e % 8 == 6)
+                *reinterpret_cast<uint4 *>(low + (((4 * k + e / 8) ^ (row & 7)) << 4)) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
             }
             lf_tmem_st16(tP + 16 * k, pw);
           }
         }
         lf_tmem_wait_st();
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       } else if (c > 0) {
         // A warp without rows must not arrive for this tile while the others
         // still owe the last one: its arrival would complete their phase.

@@ -1,0 +1,101 @@
+"""GPU tests of the paged decode's arithmetic where its kernels differ: how
+probabilities enter the product with V, infinite values, far scores.  Every
+case runs on each kernel of its type (PATHS names shapes that reach them)."""
+import math
+
+import numpy as np
+import pytest
+
+from sparse_sliding_window_b200 import lf_attn as L
+from tests import paged_ref as R
+from tests.test_paged_gpu import Cache, _reference
+
+pytestmark = pytest.mark.gpu
+
+# B, H, Hkv, prefix, length of the own rows
+PATHS = {
+    "cluster": (2, 4, 2, 0, 220),
+    "cluster, wide group": (2, 40, 2, 0, 220),
+    "runs": (40, 4, 2, 0, 220),
+    "runs, wide group": (80, 20, 1, 0, 220),
+    "direct prefix": (2, 2, 1, 200, 20),
+    "prefix, few rows": (20, 2, 2, 220, 7),
+    "prefix, 32 rows": (26, 26, 26, 220, 7),
+    "prefix, 40 rows": (20, 4, 2, 220, 7),
+    "prefix, many rows": (40, 40, 40, 220, 3),
+    "prefix, many rows in two blocks": (70, 40, 20, 220, 3),
+}
+
+
+def _fill(c, rows_of, channel, values, which):
+    """values[i] into a channel (or all: slice) of K or V at the i-th row of every sequence and of the prefix."""
+    import torch
+    pool = c.k if which == "k" else c.v
+    val = torch.as_tensor(np.asarray(values, np.float32), device="cuda").to(pool.dtype)
+    tables = [(c.table[b], int(n)) for b, n in enumerate(c.lengths)] + [(c.prefix_table, c.prefix)]
+    for table, n in tables:
+        if n == 0:
+            continue
+        at = torch.as_tensor(table[np.arange(n) // c.page].astype(np.int64), device="cuda")
+        slot = torch.arange(n, device="cuda") % c.page
+        x = val[rows_of(n)]
+        if isinstance(channel, int):
+            pool[at, :, slot, channel] = x[:, None].expand(n, c.Hkv)
+        else:
+            pool[at, :, slot] = x[:, None, None].expand(n, c.Hkv, 64)
+
+
+def _decode(c, q, H, window=-1, scale=0.0):
+    import torch
+    o = torch.full(q.shape, float("nan"), dtype=q.dtype, device="cuda")
+    lse = torch.full(q.shape[:2], float("nan"), device="cuda")
+    p = c.params(H, window, None, scale)
+    ws = L.paged_workspace(p)
+    L.lf_paged_decode(p, q, c.k, c.v, c.t_table, c.t_lengths, o, lse, ws, prefix_table=c.t_prefix)
+    L.lf_attn_status(ws)
+    return o, lse
+
+
+def _one_channel_query(B, H, dtype):
+    import torch
+    q = torch.zeros(B, H, 64, dtype=R.torch_dtype(dtype), device="cuda")
+    q[..., 0] = 1
+    return q
+
+
+def _worst_probability(dtype):
+    """A key x (score -x/8 against a query of 1) whose exp(-x/8) lies as far
+    between two 16-bit numbers as any of a grid, and that probability."""
+    import torch
+    best = (0.0, None, None)
+    for i in range(32, 64):
+        x = i / 16
+        p = math.exp(-x / 8)
+        off = abs(float(torch.tensor(p, dtype=torch.float64).to(R.torch_dtype(dtype)).double()) - p) / p
+        best = max(best, (off, x, p))
+    return best
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("path", PATHS)
+def test_probabilities_are_not_rounded_to_16_bits(path, dtype):
+    """Two groups of keys, probability 1 and value +1, probability p and value
+    -1, whose sums nearly cancel: a rounding of p to 16 bits would stand in the
+    output alone, far above the output's own rounding.  Two 16-bit numbers hold
+    p to within the square of a step (twice half a step each)."""
+    B, H, Hkv, prefix, n = PATHS[path]
+    off, x, p = _worst_probability(dtype)
+    c = Cache(901, dtype, B, Hkv, 16, [n] * B, prefix)
+    plus = round(32 * p / (1 + p))                       # of every 32 keys, spread over them
+    first = [(i * plus) % 32 < plus for i in range(32)]
+    assert sum(first) == plus
+    _fill(c, lambda m: np.arange(m) % 32, 0, [0.0 if f else -x for f in first], "k")
+    _fill(c, lambda m: np.arange(m) % 32, None, [1.0 if f else -1.0 for f in first], "v")
+    q = _one_channel_query(B, H, dtype)
+    o, lse = _decode(c, q, H)
+    half = R.half_step(dtype)
+    ref, rl, to, tl = _reference(c, q, H, -1, None, 0.125, (2 * half) ** 2)
+    # what is to be seen: p rounded to 16 bits moves the output by about half of that rounding
+    assert 0.45 * off > 1.2 * (to.max() + half * np.abs(ref).max())
+    R.check("o", R.f64(o), ref, to + half * (np.abs(ref) + to))
+    R.check("lse", R.f64(lse), rl, tl)
