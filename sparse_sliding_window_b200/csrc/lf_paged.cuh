@@ -128,8 +128,10 @@ __device__ __forceinline__ LfPair lf_add2(LfPair a, LfPair b) {
 // towards zero and, in `low`, what the cut left (together within the square of
 // a step of p), so that the output's only rounding to 16 bits is its last.
 // With one number the error of a bf16 output against 64 bits is 0.0023 of its
-// norm, with two 0.0017, which is the output's own rounding.
-template <int kF16>
+// norm, with two 0.0017, which is the output's own rounding.  kPacked: packed
+// subtraction (43.0 us where single ones take 43.4 in the tensor-core prefix
+// kernel; the warp-level kernels of 32 rows would spill a register pair).
+template <int kF16, bool kPacked>
 __device__ __forceinline__ void lf_p_split(float p0, float p1, uint32_t &high, uint32_t &low) {
   float h0, h1, r0, r1;
   if (kF16) {
@@ -142,7 +144,12 @@ __device__ __forceinline__ void lf_p_split(float p0, float p1, uint32_t &high, u
     h0 = __uint_as_float(__float_as_uint(p0) & 0xffff0000u);
     h1 = __uint_as_float(__float_as_uint(p1) & 0xffff0000u);
   }
-  lf_unpair(lf_fma2(lf_pair(h0, h1), lf_pair(-1.f, -1.f), lf_pair(p0, p1)), r0, r1);
+  if (kPacked) {
+    lf_unpair(lf_fma2(lf_pair(h0, h1), lf_pair(-1.f, -1.f), lf_pair(p0, p1)), r0, r1);
+  } else {
+    r0 = p0 - h0;
+    r1 = p1 - h1;
+  }
   // `low` is at least the type's smallest positive number (below the square of
   // a step of any p that counts): 0 times an infinite value would be NaN.
   if (kF16)

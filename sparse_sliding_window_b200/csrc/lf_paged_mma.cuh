@@ -62,13 +62,6 @@ __device__ __forceinline__ void lf_mma16(float (&d)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <typename T>
-__device__ __forceinline__ uint32_t lf_pm_pack(float a, float b) {
-  uint32_t w;
-  LfIo<T>::st2(reinterpret_cast<T *>(&w), a, b);
-  return w;
-}
-
 // byte of 16-byte unit u of row r in a tile of 128-byte rows (units swizzled by row)
 __device__ __forceinline__ uint32_t lf_pm_at(int r, int u) { return r * 128 + ((u ^ (r & 7)) << 4); }
 
@@ -214,23 +207,17 @@ __device__ __forceinline__ void lf_pm_tile(const LfPmQ<MT> &qa, uint32_t sk, uin
       S.l[mt][1] += s[mt][n][2] + s[mt][n][3];
     }
   }
-  // P enters the product with V as two 16-bit numbers, the rounded value and
-  // what the rounding left (p <= 1; together within the square of half a step),
-  // so that the output is rounded once, at its end: with one number alone the
-  // error against 64 bits is 1.4 times that of the output's own rounding.  The
-  // second product costs 1 to 5% of a decode step.
+  // P enters the product with V as two 16-bit numbers; the second product costs
+  // 1 to 5% of a decode step.
 #pragma unroll
   for (int k = 0; k < 2; k++) {
     uint32_t pa[MT][4], pb[MT][4];
 #pragma unroll
     for (int mt = 0; mt < MT; mt++)
 #pragma unroll
-      for (int i = 0; i < 4; i++) {
-        const float p0 = s[mt][2 * k + i / 2][2 * (i % 2)], p1 = s[mt][2 * k + i / 2][2 * (i % 2) + 1];
-        pa[mt][i] = lf_pm_pack<T>(p0, p1);
-        const float2 r = LfIo<T>::ld2(reinterpret_cast<const T *>(&pa[mt][i]));
-        pb[mt][i] = lf_pm_pack<T>(p0 - r.x, p1 - r.y);
-      }
+      for (int i = 0; i < 4; i++)
+        lf_p_split<std::is_same<T, __half>::value, false>(
+            s[mt][2 * k + i / 2][2 * (i % 2)], s[mt][2 * k + i / 2][2 * (i % 2) + 1], pa[mt][i], pb[mt][i]);
 #pragma unroll
     for (int n = 0; n < 8; n += 2) {
       uint32_t b[4];  // 16 keys x 16 channels, transposed

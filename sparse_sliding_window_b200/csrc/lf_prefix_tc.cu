@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(LF_PT_THREADS, 1) lf_prefix_tc_kernel(const __
               p0 = lf_ex2(p0);
               p1 = lf_ex2(p1);
               sums[e / 2 % 2] = lf_add2(sums[e / 2 % 2], lf_pair(p0, p1));
-              lf_p_split<kF16>(p0, p1, pw[e / 2], pl[e / 2 % 4]);
+              lf_p_split<kF16, true>(p0, p1, pw[e / 2], pl[e / 2 % 4]);
               if (e % 8 == 6)
                 *reinterpret_cast<uint4 *>(low + (((4 * k + e / 8) ^ (row & 7)) << 4)) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
             }
@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(LF_PT_THREADS, 1) lf_prefix_tc_kernel(const __
               const float p0 = (w[k] >> e & 1u) ? lf_ex2(fmaf(__uint_as_float(v[k][e]), sl2, -m_ref)) : 0.f;
               const float p1 = (w[k] >> e & 2u) ? lf_ex2(fmaf(__uint_as_float(v[k][e + 1]), sl2, -m_ref)) : 0.f;
               l += p0 + p1;
-              lf_p_split<kF16>(p0, p1, pw[e / 2], pl[e / 2 % 4]);
+              lf_p_split<kF16, true>(p0, p1, pw[e / 2], pl[e / 2 % 4]);
               if (e % 8 == 6)
                 *reinterpret_cast<uint4 *>(low + (((4 * k + e / 8) ^ (row & 7)) << 4)) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
             }

@@ -99,3 +99,44 @@ def test_probabilities_are_not_rounded_to_16_bits(path, dtype):
     assert 0.45 * off > 1.2 * (to.max() + half * np.abs(ref).max())
     R.check("o", R.f64(o), ref, to + half * (np.abs(ref) + to))
     R.check("lse", R.f64(lse), rl, tl)
+
+
+@pytest.mark.parametrize("dtype", R.DTYPES)
+@pytest.mark.parametrize("path", PATHS)
+def test_infinite_values_of_attended_keys(path, dtype):
+    """An infinity among the attended values is the output's infinity, whatever
+    the key's probability is (1 for a sequence of one key); infinities of both
+    signs are NaN; the other channels are what they are without them."""
+    import torch
+    B, H, Hkv, prefix, n = PATHS[path]
+    c = Cache(902, dtype, B, Hkv, 16, [1] + [n] * (B - 1), prefix)
+    q = _one_channel_query(B, H, dtype)
+    q += _normal_like(c, q) / 4
+    tables = [(c.table[b], int(m)) for b, m in enumerate(c.lengths)] + [(c.prefix_table, prefix)]
+    where = [(3, 0, math.inf), (4, 1, -math.inf), (5, 0, math.inf), (5, 1, -math.inf)]
+    for table, m in tables:
+        for ch, row, x in where:
+            if row < m:
+                c.v[table[row // 16], :, row % 16, ch] = x
+    o, lse = _decode(c, q, H)
+    assert (o[..., 3] == math.inf).all()
+    two = o[1:] if not prefix else o
+    assert (two[..., 4] == -math.inf).all() and torch.isnan(two[..., 5]).all()
+    if not prefix:
+        assert (o[0, :, 5] == math.inf).all() and torch.isfinite(o[0, :, 4]).all()
+    clean = torch.where(torch.isinf(c.v), torch.zeros_like(c.v), c.v)
+    o0, lse0 = _decode(_with(c, v=clean), q, H)
+    rest = [ch for ch in range(64) if ch not in (3, 4, 5)]
+    assert torch.equal(o[..., rest], o0[..., rest]) and torch.equal(lse, lse0)
+
+
+def _normal_like(c, q):
+    import torch
+    return torch.from_numpy(c.rng.standard_normal(tuple(q.shape)).astype(np.float32)).to("cuda", q.dtype)
+
+
+def _with(c, **kw):
+    import copy
+    d = copy.copy(c)
+    d.__dict__.update(kw)
+    return d
