@@ -733,7 +733,7 @@ __global__ void __launch_bounds__(128, MT == 1 ? 3 : 2)
       if (C.tile + 1 == C.nt || i + 1 == end) {
         const int ustart = i - C.tile, uend = ustart + C.nt;  // the unit in the list
         const bool whole = first == 0 && C.tile + 1 == C.nt;
-        lf_pm_sum<MT>(S);
+        lf_pm_sum<T, MT>(S);
         if (prefix && whole) asm volatile("griddepcontrol.wait;" ::: "memory");  // the prefix partials
         const size_t orow = (size_t)C.b * P.H + C.hk * P.G + g0;
         const size_t prow = ((size_t)C.hk * P.B + C.b) * P.G + g0;

@@ -123,6 +123,14 @@ __device__ __forceinline__ LfPair lf_add2(LfPair a, LfPair b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+__device__ __forceinline__ LfPair lf_mul2(LfPair a, LfPair b) {
+  LfPair r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+#define LF_P_UP 7
+#define LF_P_SCALE ((float)(1 << LF_P_UP))
 
 // Two probabilities as two 16-bit numbers each, for the product with V: p cut
 // towards zero and, in `low`, what the cut left (together within the square of
@@ -131,10 +139,19 @@ __device__ __forceinline__ LfPair lf_add2(LfPair a, LfPair b) {
 // norm, with two 0.0017, which is the output's own rounding.  kPacked: packed
 // subtraction (43.0 us where single ones take 43.4 in the tensor-core prefix
 // kernel; the warp-level kernels of 32 rows would spill a register pair).
+// f16: p enters 2^LF_P_UP times as large, so that numbers down to 2^-31 of the
+// largest one are held (2^-24 is f16's smallest; p <= 2^8 stays below 65504);
+// the output's owner takes the factor out again.
 template <int kF16, bool kPacked>
 __device__ __forceinline__ void lf_p_split(float p0, float p1, uint32_t &high, uint32_t &low) {
   float h0, h1, r0, r1;
   if (kF16) {
+    if (kPacked) {
+      lf_unpair(lf_mul2(lf_pair(p0, p1), lf_pair(LF_P_SCALE, LF_P_SCALE)), p0, p1);
+    } else {
+      p0 *= LF_P_SCALE;
+      p1 *= LF_P_SCALE;
+    }
     asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(high) : "f"(p1), "f"(p0));
     const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&high));
     h0 = h.x;
@@ -150,8 +167,8 @@ __device__ __forceinline__ void lf_p_split(float p0, float p1, uint32_t &high, u
     r0 = p0 - h0;
     r1 = p1 - h1;
   }
-  // `low` is at least the type's smallest positive number (below the square of
-  // a step of any p that counts): 0 times an infinite value would be NaN.
+  // `low` is at least the type's smallest positive number (2^-31 of the largest
+  // p, or less): 0 times an infinite value would be NaN.
   if (kF16)
     asm("{\n\t.reg .b32 r;\n\tcvt.rn.f16x2.f32 r, %1, %2;\n\tmax.f16x2 %0, r, %3;\n\t}"
         : "=r"(low) : "f"(r1), "f"(r0), "r"(0x00010001u));

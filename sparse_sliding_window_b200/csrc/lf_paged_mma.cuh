@@ -66,7 +66,8 @@ __device__ __forceinline__ void lf_mma16(float (&d)[4], const uint32_t (&a)[4], 
 __device__ __forceinline__ uint32_t lf_pm_at(int r, int u) { return r * 128 + ((u ^ (r & 7)) << 4); }
 
 // A warp's state: rows 16 mt + g and + 8 (g = lane / 4), output channels
-// 8n + 2t, + 1 (t = lane % 4) in acc[mt][n].
+// 8n + 2t, + 1 (t = lane % 4) in acc[mt][n] (f16: LF_P_SCALE times as large
+// until lf_pm_sum).
 template <int MT> struct LfPmState {
   float acc[MT][8][4], m[MT][2], l[MT][2];  // l: this thread's keys only, until lf_pm_sum
 };
@@ -233,14 +234,20 @@ __device__ __forceinline__ void lf_pm_tile(const LfPmQ<MT> &qa, uint32_t sk, uin
   }
 }
 
-// The row sums over the row's four threads.
-template <int MT> __device__ __forceinline__ void lf_pm_sum(LfPmState<MT> &S) {
+// The row sums over the row's four threads; f16's factor out of the outputs.
+template <typename T, int MT> __device__ __forceinline__ void lf_pm_sum(LfPmState<MT> &S) {
 #pragma unroll
-  for (int mt = 0; mt < MT; mt++)
+  for (int mt = 0; mt < MT; mt++) {
 #pragma unroll
     for (int u = 0; u < 2; u++)
 #pragma unroll
       for (int w = 1; w < 4; w <<= 1) S.l[mt][u] += __shfl_xor_sync(0xffffffffu, S.l[mt][u], w);
+    if (std::is_same<T, __half>::value)
+#pragma unroll
+      for (int n = 0; n < 8; n++)
+#pragma unroll
+        for (int i = 0; i < 4; i++) S.acc[mt][n][i] *= 1.f / LF_P_SCALE;
+  }
 }
 
 // Tiles tile0, tile0 + tstep, ... of the keys; ring: the four warps' stages.
@@ -276,7 +283,7 @@ __device__ __forceinline__ void lf_pm_attend(const LfPagedDev &P, const LfPmKeys
     for (int i = 0; i + 1 < LF_PM_STAGES; i++) ok[i] = ok[i + 1];
     st = st + 1 == LF_PM_STAGES ? 0 : st + 1;
   }
-  lf_pm_sum<MT>(S);
+  lf_pm_sum<T, MT>(S);
   lf_cp_wait<0>();
   __syncwarp();
 }

@@ -470,8 +470,9 @@ __global__ void __launch_bounds__(LF_PT_THREADS, 1) lf_prefix_tc_kernel(const __
           uint32_t ov[32];
           lf_tmem_ld32_nowait(tq + LF_PT_TO(k) + 32 * g, ov);
           lf_tmem_wait_ld_regs(ov);
+          const float fo = kF16 ? f * (1.f / LF_P_SCALE) : f;
 #pragma unroll
-          for (int e = 0; e < 32; e++) acc[e] = fmaf(__uint_as_float(ov[e]), f, acc[e]);
+          for (int e = 0; e < 32; e++) acc[e] = fmaf(__uint_as_float(ov[e]), fo, acc[e]);
         }
       }
       // through shared memory (the ring is done with), so that whole rows leave

@@ -140,3 +140,25 @@ def _with(c, **kw):
     d = copy.copy(c)
     d.__dict__.update(kw)
     return d
+
+
+@pytest.mark.parametrize("dtype", R.DTYPES)
+@pytest.mark.parametrize("path", PATHS)
+def test_many_small_probabilities_add_up(path, dtype):
+    """Every 16th key has score 0 and value 0, the others probability 2^-26 of
+    it and value 64: the output is what the small ones add up to."""
+    B, H, Hkv, prefix, n = PATHS[path]
+    c = Cache(903, dtype, B, Hkv, 16, [n] * B, prefix)
+    x = 26 * math.log(2) * 8                      # 144.2: rounded by the type, the reference takes it as it is then
+    _fill(c, lambda m: np.arange(m) % 16, 0, [0.0] + [-x] * 15, "k")
+    _fill(c, lambda m: np.arange(m) % 16, None, [0.0] + [64.0] * 15, "v")
+    q = _one_channel_query(B, H, dtype)
+    o, lse = _decode(c, q, H)
+    half = R.half_step(dtype)
+    ref, rl, to, tl = _reference(c, q, H, -1, None, 0.125, (2 * half) ** 2 if dtype != "f32" else 0.0)
+    # f16: a probability is held to 2^-31 of the largest one (of which there is one in sixteen keys), the
+    # output's own spacing below the smallest normal number is 2^-24
+    floor = 16 * 64 * 2.0 ** -31 + 2.0 ** -25 if dtype == "f16" else 0.0
+    assert np.abs(ref).min() > 16 * floor
+    R.check("o", R.f64(o), ref, to + floor + half * (np.abs(ref) + to))
+    R.check("lse", R.f64(lse), rl, tl)
