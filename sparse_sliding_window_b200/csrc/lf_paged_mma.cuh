@@ -158,6 +158,16 @@ __device__ __forceinline__ void lf_pm_tile(const LfPmQ<MT> &qa, uint32_t sk, uin
       }
     }
   }
+  // The scaled scores are rounded before the maximum is taken from them, and not
+  // inside one operation with that subtraction: the largest exponent is 0 then,
+  // however large the scores are (beyond 2^24 the difference to the rounded
+  // maximum would be whole powers of two, and p infinite or 0 in every key).
+#pragma unroll
+  for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+    for (int n = 0; n < 4; n++)
+#pragma unroll
+      for (int i = 0; i < 4; i++) s[mt][n][i] = __fmul_rn(s[mt][n][i], scale_log2);
   if (ok != 0xffffffffu) {
 #pragma unroll
     for (int n = 0; n < 4; n++)
@@ -180,8 +190,8 @@ __device__ __forceinline__ void lf_pm_tile(const LfPmQ<MT> &qa, uint32_t sk, uin
       M0 = fmaxf(M0, __shfl_xor_sync(0xffffffffu, M0, w));
       M1 = fmaxf(M1, __shfl_xor_sync(0xffffffffu, M1, w));
     }
-    M0 = fmaxf(S.m[mt][0], M0 * scale_log2);  // the scale is positive
-    M1 = fmaxf(S.m[mt][1], M1 * scale_log2);
+    M0 = fmaxf(S.m[mt][0], M0);
+    M1 = fmaxf(S.m[mt][1], M1);
     if (__any_sync(0xffffffffu, M0 > S.m[mt][0] || M1 > S.m[mt][1])) {
       const float f0 = lf_part_scale(S.m[mt][0], M0), f1 = lf_part_scale(S.m[mt][1], M1);
       S.m[mt][0] = M0;
@@ -200,10 +210,10 @@ __device__ __forceinline__ void lf_pm_tile(const LfPmQ<MT> &qa, uint32_t sk, uin
     const float e0 = M0 == -INFINITY ? 0.f : M0, e1 = M1 == -INFINITY ? 0.f : M1;
 #pragma unroll
     for (int n = 0; n < 4; n++) {
-      s[mt][n][0] = lf_ex2(fmaf(s[mt][n][0], scale_log2, -e0));
-      s[mt][n][1] = lf_ex2(fmaf(s[mt][n][1], scale_log2, -e0));
-      s[mt][n][2] = lf_ex2(fmaf(s[mt][n][2], scale_log2, -e1));
-      s[mt][n][3] = lf_ex2(fmaf(s[mt][n][3], scale_log2, -e1));
+      s[mt][n][0] = lf_ex2(s[mt][n][0] - e0);
+      s[mt][n][1] = lf_ex2(s[mt][n][1] - e0);
+      s[mt][n][2] = lf_ex2(s[mt][n][2] - e1);
+      s[mt][n][3] = lf_ex2(s[mt][n][3] - e1);
       S.l[mt][0] += s[mt][n][0] + s[mt][n][1];
       S.l[mt][1] += s[mt][n][2] + s[mt][n][3];
     }

@@ -64,6 +64,7 @@ static_assert(8 * 32 * 36 * 4 <= LF_PT_MISC - LF_PT_K(0), "staging");
 // A row's reference may lag its running maximum by this much (log2): p stays
 // below 2^8 and O is rescaled only when a score is far above everything before.
 #define LF_PT_LAG 8.f
+#define LF_PT_NEAR 1048576.f
 
 // Warp-uniform bounded wait, inlined: the softmax warps hold a row of S in
 // registers across it, which a call would push to local memory.
@@ -366,7 +367,7 @@ __global__ void __launch_bounds__(LF_PT_THREADS, 1) lf_prefix_tc_kernel(const __
 #pragma unroll
             for (int e = 0; e < 32; e++) mx[k] = fmaxf(mx[k], (w[k] >> e & 1u) ? __uint_as_float(v[k][e]) : -INFINITY);
         }
-        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+        const float mt = __fmul_rn(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), sl2);
         if (c > 0) {  // the stream's last product has read P and is in O
           ok = lf_pt_wait(bar + LF_PT_PV_DONE(g), (c - 1) & 1, abort_flag, P.status, 51);
           if (!ok) break;
@@ -377,8 +378,8 @@ __global__ void __launch_bounds__(LF_PT_THREADS, 1) lf_prefix_tc_kernel(const __
           m_ref = mt;
           fresh = false;
         }
-        if (__any_sync(0xffffffffu, !fresh && mt > m_ref + LF_PT_LAG)) {
-          const bool up = !fresh && mt > m_ref + LF_PT_LAG;
+        const bool up = !fresh && mt - m_ref > LF_PT_LAG;
+        if (__any_sync(0xffffffffu, up)) {
           const float f = up ? lf_ex2(m_ref - mt) : 1.f;
           if (up) m_ref = mt;
           l *= f;
@@ -396,7 +397,11 @@ __global__ void __launch_bounds__(LF_PT_THREADS, 1) lf_prefix_tc_kernel(const __
         // (One number alone: 128 x 16/4 heads on 16384 rows 38.4 us instead of
         // 43.0, 64 x 12 heads on 4096 rows 25.8 instead of 27.3.)
         uint8_t *low = lf_smem_raw + LF_PT_L(g) + row * 128;
-        if (all) {
+        // The scaling and the subtraction of the reference are one operation where
+        // the reference's own rounding is far below 1 (at most 2^-4).  Beyond, the
+        // scaled score is rounded first, as the reference was: the difference would
+        // else be whole powers of two, and p infinite or 0 in every key.
+        if (all && __all_sync(0xffffffffu, fabsf(m_ref) < LF_PT_NEAR)) {
           LfPair sums[2] = {lf_pair(0.f, 0.f), lf_pair(0.f, 0.f)};
           const LfPair refp = lf_pair(-m_ref, -m_ref);
 #pragma unroll
@@ -424,8 +429,8 @@ __global__ void __launch_bounds__(LF_PT_THREADS, 1) lf_prefix_tc_kernel(const __
             uint32_t pw[16], pl[4];
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-              const float p0 = (w[k] >> e & 1u) ? lf_ex2(fmaf(__uint_as_float(v[k][e]), sl2, -m_ref)) : 0.f;
-              const float p1 = (w[k] >> e & 2u) ? lf_ex2(fmaf(__uint_as_float(v[k][e + 1]), sl2, -m_ref)) : 0.f;
+              const float p0 = (w[k] >> e & 1u) ? lf_ex2(__fmul_rn(__uint_as_float(v[k][e]), sl2) - m_ref) : 0.f;
+              const float p1 = (w[k] >> e & 2u) ? lf_ex2(__fmul_rn(__uint_as_float(v[k][e + 1]), sl2) - m_ref) : 0.f;
               l += p0 + p1;
               lf_p_split<kF16, true>(p0, p1, pw[e / 2], pl[e / 2 % 4]);
               if (e % 8 == 6)

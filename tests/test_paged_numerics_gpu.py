@@ -162,3 +162,34 @@ def test_many_small_probabilities_add_up(path, dtype):
     assert np.abs(ref).min() > 16 * floor
     R.check("o", R.f64(o), ref, to + floor + half * (np.abs(ref) + to))
     R.check("lse", R.f64(lse), rl, tl)
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("dtype", R.DTYPES)
+@pytest.mark.parametrize("path", PATHS)
+def test_far_scores_stay_finite(path, dtype, sign):
+    """Scores of 2^34 (f16) and 2^80: one key, row 1 of every sequence, is above
+    all others by more than the scores' roundings and takes the whole
+    probability."""
+    B, H, Hkv, prefix, n = PATHS[path]
+    c = Cache(904, dtype, B, Hkv, 16, [n] * B, prefix)
+    top = 2.0 ** 14 if dtype == "f16" else 2.0 ** 40
+    # multiples of top that the types hold and whose products need rounding; row 1 of a sequence outweighs the rest
+    values = [1.0 + (i % 7) / 8 for i in range(32)]
+    values = [top * (a if sign > 0 else a + 1) for a in values]
+    for ch in range(64):
+        _fill(c, lambda m: np.arange(m) % 32, ch, values, "k")
+    win = top * (2.5 if sign > 0 else 0.625)
+    for b in range(B):
+        c.k[c.table[b, 0], :, 1] = win
+    q = _one_channel_query(B, H, dtype)
+    q[:] = sign * 1.1 * top
+    o, lse = _decode(c, q, H)
+    half = R.half_step(dtype)
+    v = R.f64(c.v)
+    s = float(q[0, 0, 0].double()) * win * 64 * 0.125
+    for b in range(B):
+        want = np.repeat(v[c.table[b, 0], :, 1], H // Hkv, axis=0)
+        R.check("o", R.f64(o[b]), want, 2 * half * np.abs(want))
+        # a float32 sum of 64 equal products and two scalings
+        R.check("lse", R.f64(lse[b]), np.full(H, s), 70 * 2.0 ** -24 * abs(s))
