@@ -193,3 +193,71 @@ def test_far_scores_stay_finite(path, dtype, sign):
         R.check("o", R.f64(o[b]), want, 2 * half * np.abs(want))
         # a float32 sum of 64 equal products and two scalings
         R.check("lse", R.f64(lse[b]), np.full(H, s), 70 * 2.0 ** -24 * abs(s))
+
+
+@pytest.mark.parametrize("rise", [40, 44, 45.5, 60, 200])
+@pytest.mark.parametrize("dtype", R.DTYPES)
+@pytest.mark.parametrize("shape", [(40, 40, 40, 1500), (64, 64, 32, 1300), (20, 20, 20, 900)])
+def test_prefix_scores_that_rise(shape, dtype, rise):
+    """Scores that rise every 192 keys by about 8 in base 2 (44.4 in this
+    channel), by less and by more, for some queries at half the rate, falling,
+    or not at all: what a kernel has added up so far is scaled down, or may
+    stay, and every chunk of the prefix has its own reference."""
+    import torch
+    B, H, Hkv, prefix = shape
+    c = Cache(905, dtype, B, Hkv, 32, [3] * B, prefix)
+    step = np.arange(prefix) // 192
+    for j in range(prefix):
+        c.k[int(c.prefix_table[j // 32]), :, j % 32, 0] = float(rise * (step[j] % 4))
+    q = _normal_like(c, torch.zeros(B, H, 64)).to(R.torch_dtype(dtype))
+    q[..., 0] = torch.from_numpy(c.rng.choice([1.0, 1.0, 0.5, 0.0, -1.0], (B, H))).to("cuda", q.dtype)
+    if rise >= 60:   # from a tile of 64 keys to the third after it, in the first head of a query that follows the rise
+        b = int(np.flatnonzero(R.f64(q[:, 0, 0]) == 1)[0])
+        top = (R.cache_rows(R.f64(c.k), c.prefix_table, prefix, 0) @ R.f64(q[b, 0]) / 8 * np.log2(np.e))[:768].reshape(12, 64).max(1)
+        assert (top[3:] - top[:-3]).min() > 8
+    o, lse = _decode(c, q, H)
+    half = R.half_step(dtype)
+    some = sorted(c.rng.choice(B, 12, replace=False).tolist())
+    d = _with(c, lengths=c.lengths[some], table=c.table[some])
+    ref, rl, to, tl = _reference(d, q[some], H, -1, None, 0.125, (2 * half) ** 2 if dtype != "f32" else 0.0)
+    floor = 64 * 8 * 2.0 ** -31 if dtype == "f16" else 0.0
+    R.check("o", R.f64(o[some]), ref, to + floor + half * (np.abs(ref) + to))
+    R.check("lse", R.f64(lse[some]), rl, tl)
+
+
+@pytest.mark.parametrize("dtype", R.DTYPES)
+@pytest.mark.parametrize("B,H,Hkv,prefix", [(3, 4, 2, 100), (20, 4, 4, 300), (40, 4, 2, 300), (30, 40, 2, 200)])
+def test_dilated_window_behind_a_prefix(B, H, Hkv, prefix, dtype):
+    c = Cache(906, dtype, B, Hkv, 16, [(b * 37) % 150 for b in range(B)], prefix)
+    q = _normal_like(c, _one_channel_query(B, H, dtype))
+    dil = [1 + 2 * (h % 2) for h in range(Hkv)]
+    o, lse = _decode_dilated(c, q, H, 20, dil)
+    half = R.half_step(dtype)
+    ref, rl, to, tl = _reference(c, q, H, 20, dil, 0.125, (2 * half) ** 2 if dtype != "f32" else 0.0)
+    R.check("o", R.f64(o), ref, to + 2.0 ** -25 + half * (np.abs(ref) + to))
+    R.check("lse", R.f64(lse), rl, tl)
+
+
+def _decode_dilated(c, q, H, window, dil):
+    import torch
+    o, lse = torch.full_like(q, float("nan")), torch.full(q.shape[:2], float("nan"), device="cuda")
+    p = c.params(H, window, dil)
+    ws = L.paged_workspace(p)
+    L.lf_paged_decode(p, q, c.k, c.v, c.t_table, c.t_lengths, o, lse, ws, prefix_table=c.t_prefix)
+    L.lf_attn_status(ws)
+    return o, lse
+
+
+@pytest.mark.parametrize("dtype", R.DTYPES)
+@pytest.mark.parametrize("B,H,Hkv,prefix", [(1100, 2, 1, 150), (1100, 20, 1, 70), (300, 128, 128, 0)])
+def test_batches_larger_than_the_run_list(B, H, Hkv, prefix, dtype):
+    """More than 1024 sequences, behind a prefix, and more than 32768 (sequence, head) units."""
+    c = Cache(907, dtype, B, Hkv, 16, [b % 24 for b in range(B)], prefix)
+    q = _normal_like(c, _one_channel_query(B, H, dtype))
+    o, lse = _decode(c, q, H)
+    half = R.half_step(dtype)
+    some = list(range(0, B, max(1, B * H // 2200)))
+    d = _with(c, lengths=c.lengths[some], table=c.table[some])
+    ref, rl, to, tl = _reference(d, q[some], H, -1, None, 0.125, (2 * half) ** 2 if dtype != "f32" else 0.0)
+    R.check("o", R.f64(o[some]), ref, to + 2.0 ** -25 + half * (np.abs(ref) + to))
+    R.check("lse", R.f64(lse[some]), rl, tl)
