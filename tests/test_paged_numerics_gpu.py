@@ -211,10 +211,12 @@ def test_prefix_scores_that_rise(shape, dtype, rise):
         c.k[int(c.prefix_table[j // 32]), :, j % 32, 0] = float(rise * (step[j] % 4))
     q = _normal_like(c, torch.zeros(B, H, 64)).to(R.torch_dtype(dtype))
     q[..., 0] = torch.from_numpy(c.rng.choice([1.0, 1.0, 0.5, 0.0, -1.0], (B, H))).to("cuda", q.dtype)
-    if rise >= 60:   # from a tile of 64 keys to the third after it, in the first head of a query that follows the rise
+    if rise >= 60:
+        # from a tile of 64 keys to the third after it, in the first head of a query that follows the rise: the
+        # channel's 10.8 or 36 in base 2, more or less the difference of the other channels' maxima (below 10)
         b = int(np.flatnonzero(R.f64(q[:, 0, 0]) == 1)[0])
         top = (R.cache_rows(R.f64(c.k), c.prefix_table, prefix, 0) @ R.f64(q[b, 0]) / 8 * np.log2(np.e))[:768].reshape(12, 64).max(1)
-        assert (top[3:] - top[:-3]).min() > 8
+        assert (top[3:] - top[:-3]).max() > 8 and (rise < 200 or (top[3:] - top[:-3]).min() > 8)
     o, lse = _decode(c, q, H)
     half = R.half_step(dtype)
     some = sorted(c.rng.choice(B, 12, replace=False).tolist())
