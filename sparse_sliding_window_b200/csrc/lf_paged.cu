@@ -25,6 +25,22 @@ __device__ __forceinline__ void lf_pd_write(T *o, float *lse, size_t row, int c,
   if (lse && c == 0) lse[row] = none ? -INFINITY : (M + log2f(L)) * LF_LN2;
 }
 
+// Before a decode kernel reads the call's inputs.  Behind a prefix kernel they
+// are already complete: every block of that kernel waited for its own
+// predecessors before it let this one start.  What those wrote is in L2, but the
+// wait that would make it visible here comes only with the prefix's parts; the
+// fence keeps loads behind it from hitting lines that L1 held before (and the
+// inputs are not read through the read-only path).  Measured, nothing / fence /
+// reads past L1 / waiting for the prefix kernel, in us: 64 x 12 heads on 4096
+// rows 27.5 / 27.9 / 29.4 / 29.4, 128 x 16/4 heads on 16384 rows 43.0 / 43.4 /
+// 45.1 / 46.4, f32 40 x 8 heads on 1000 rows 22.9 / 23.4 / 23.0 / 29.0.
+__device__ __forceinline__ void lf_pd_begin(bool prefix) {
+  if (prefix)
+    asm volatile("fence.acq_rel.gpu;" ::: "memory");
+  else
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // ===================================================== decode kernel (f32)
 
 #define LF_PD_WARPS 4
@@ -38,9 +54,8 @@ __device__ __forceinline__ void lf_pd_write(T *o, float *lse, size_t row, int c,
 // registers, shared memory and distributed shared memory.
 template <typename T, int GT>
 __global__ void __launch_bounds__(LF_PD_WARPS * 32)
-    lf_paged_decode_kernel(const __grid_constant__ LfPagedDev P, const T *__restrict__ q,
-                           const T *__restrict__ kp, const T *__restrict__ vp, T *__restrict__ o,
-                           float *__restrict__ lse, int ngroups, int cl) {
+    lf_paged_decode_kernel(const __grid_constant__ LfPagedDev P, const T *q, const T *kp, const T *vp, T *o,
+                           float *lse, int ngroups, int cl) {
   constexpr int N = LfVec<T>::N;
   constexpr int LPR = LF_HD / N;        // lanes per row
   constexpr int SUB = 32 / LPR;         // rows per warp load
@@ -48,9 +63,7 @@ __global__ void __launch_bounds__(LF_PD_WARPS * 32)
   __shared__ float s_m[LF_PD_WARPS][GT], s_l[LF_PD_WARPS][GT], s_acc[LF_PD_WARPS][GT][LF_HD];
   extern __shared__ float s_cl[];  // CTA 0 of a cluster: [cl][GT] m, l and [cl][GT][64]
   const bool prefix = P.nch > 0;  // parts of a prefix kernel to add
-  // Behind a prefix kernel the call's inputs are already complete: every block
-  // of that kernel waited for its own predecessors before it let this one start.
-  if (!prefix) asm volatile("griddepcontrol.wait;" ::: "memory");
+  lf_pd_begin(prefix);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   cg::cluster_group cluster = cg::this_cluster();
   const int crank = cl > 1 ? (int)cluster.block_rank() : 0;
@@ -431,9 +444,7 @@ __global__ void __launch_bounds__(128, 2)
   extern __shared__ __align__(16) char smem_raw[];
   __shared__ float s_m[4][16], s_l[4][16];
   const bool prefix = P.nch > 0;  // parts of a prefix kernel to add
-  // Behind a prefix kernel the call's inputs are already complete: every block
-  // of that kernel waited for its own predecessors before it let this one start.
-  if (!prefix) asm volatile("griddepcontrol.wait;" ::: "memory");
+  lf_pd_begin(prefix);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   cg::cluster_group cluster = cg::this_cluster();
   const int crank = cl > 1 ? (int)cluster.block_rank() : 0;
@@ -598,7 +609,7 @@ __global__ void __launch_bounds__(128, MT == 1 ? 3 : 2)
   __shared__ int s_warp[4], s_last, s_at[2];
   __shared__ LfPdRun s_cut[2];
   const bool prefix = P.nch > 0;  // parts of a prefix kernel to add
-  if (!prefix) asm volatile("griddepcontrol.wait;" ::: "memory");  // as in lf_paged_mma_kernel
+  lf_pd_begin(prefix);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int gmax = min(RB, P.G), wrows = min(16, P.G);

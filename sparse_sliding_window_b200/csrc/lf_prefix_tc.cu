@@ -142,6 +142,7 @@ __global__ void __launch_bounds__(LF_PT_THREADS, 1) lf_prefix_tc_kernel(const __
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (sbase & 1023u) {  // 128-byte swizzled tiles need it
     if (tid == 0) lf_set_status(P.status, LF_ERR_UNSUPPORTED, 9000);
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the decode kernel relies on it
     return;
   }
   if (tid == 0) {

@@ -263,3 +263,49 @@ def test_batches_larger_than_the_run_list(B, H, Hkv, prefix, dtype):
     ref, rl, to, tl = _reference(d, q[some], H, -1, None, 0.125, (2 * half) ** 2 if dtype != "f32" else 0.0)
     R.check("o", R.f64(o[some]), ref, to + 2.0 ** -25 + half * (np.abs(ref) + to))
     R.check("lse", R.f64(lse[some]), rl, tl)
+
+
+@pytest.mark.parametrize("dtype", R.DTYPES)
+@pytest.mark.parametrize("B,H,Hkv,prefix", [(40, 4, 2, 300), (20, 4, 4, 300), (12, 2, 2, 200), (60, 4, 2, 0)])
+def test_captured_steps_follow_what_kernels_write(B, H, Hkv, prefix, dtype):
+    """Steps in one graph, each of which changes the lengths, the queries and
+    the newest rows by kernels right before the call that reads them, are those
+    of calls that wait for one another."""
+    import torch
+    steps = 6
+    c = Cache(908, dtype, B, Hkv, 16, [40 + b % 3 for b in range(B)], prefix)
+    p, rope = c.params(H, 30), L.make_rope_params()
+    ws = L.paged_workspace(p)
+    new = [_normal_like(c, torch.zeros(steps, B, h, 64)).to(c.k.dtype) for h in (H, Hkv, Hkv)]
+    q, qo = torch.empty_like(new[0][0]), torch.empty_like(new[0][0])
+    outs = torch.zeros(steps, B, H, 64, dtype=c.k.dtype, device="cuda"), torch.zeros(steps, B, H, device="cuda")
+    start = c.t_lengths.clone()
+
+    def run(kp, vp, lengths, o, lse, wait):
+        lengths.copy_(start - steps)
+        for s in range(steps):
+            lengths.add_(1)
+            q.copy_(new[0][s])
+            L.lf_cache_append(p, rope, q, new[1][s], new[2][s], lengths, c.t_table, qo, kp, vp, ws)
+            if wait:
+                torch.cuda.synchronize()
+            L.lf_paged_decode(p, qo, kp, vp, c.t_table, lengths, o[s], lse[s], ws, prefix_table=c.t_prefix)
+            if wait:
+                torch.cuda.synchronize()
+
+    kp, vp, lengths = c.k.clone(), c.v.clone(), c.t_lengths.clone()
+    want = torch.empty_like(outs[0]), torch.empty_like(outs[1])
+    run(kp, vp, lengths, *want, True)
+    L.lf_attn_status(ws)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run(c.k, c.v, c.t_lengths, *outs, False)
+    base = [x.clone() for x in (c.k, c.v)]
+    for _ in range(20):
+        c.k.copy_(base[0])
+        c.v.copy_(base[1])
+        outs[0].zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
+    assert all(torch.equal(x.view(torch.int16), y.view(torch.int16)) for x, y in ((c.k, kp), (c.v, vp)))
