@@ -156,18 +156,6 @@ template <> struct LfIo<__half> {
   }
 };
 
-// one element, rounded to nearest even
-template <typename T> struct LfIo1;
-template <> struct LfIo1<float> {
-  static __device__ __forceinline__ void st(float *p, float a) { *p = a; }
-};
-template <> struct LfIo1<__nv_bfloat16> {
-  static __device__ __forceinline__ void st(__nv_bfloat16 *p, float a) { *p = __float2bfloat16_rn(a); }
-};
-template <> struct LfIo1<__half> {
-  static __device__ __forceinline__ void st(__half *p, float a) { *p = __float2half_rn(a); }
-};
-
 // 16-byte slice of a 64-element row: N elements of T as floats.  A row is
 // handled by 64 / N consecutive lanes (a lane group).
 template <typename T> struct LfVec;

@@ -16,6 +16,18 @@
 
 namespace cg = cooperative_groups;
 
+// one element, rounded to nearest even
+template <typename T> struct LfIo1;
+template <> struct LfIo1<float> {
+  static __device__ __forceinline__ void st(float *p, float a) { *p = a; }
+};
+template <> struct LfIo1<__nv_bfloat16> {
+  static __device__ __forceinline__ void st(__nv_bfloat16 *p, float a) { *p = __float2bfloat16_rn(a); }
+};
+template <> struct LfIo1<__half> {
+  static __device__ __forceinline__ void st(__half *p, float a) { *p = __float2half_rn(a); }
+};
+
 // Element (row g, channel c) of the newest token's output from its merged
 // state: o = a / L, lse = log of the sum, 0 and -inf where nothing was attended.
 template <typename T>
