@@ -9,6 +9,7 @@ import os
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -37,16 +38,25 @@ def needs_build() -> bool:
     return any(os.path.getmtime(s) > t for s in deps)
 
 
+def _bind_tag() -> bytes:
+    """What the module carries of the torch that it was built against."""
+    import torch
+    return ("lf_bind for torch %s." % torch.__version__).encode()
+
+
 def build_bind(force: bool = False, verbose: bool = False) -> str:
     """The Python module _lf_bind, against the installed torch and liblf_attn.so."""
     deps = [BIND_SOURCE] + [os.path.join(ROOT, "include", h) for h in ("lf_attn.h", "lf_paged.h")]
+    tag = _bind_tag()
     if not force and os.path.exists(BIND) and all(os.path.getmtime(d) <= os.path.getmtime(BIND) for d in deps):
-        return BIND
+        with open(BIND, "rb") as f:
+            if tag in f.read():
+                return BIND
     from torch.utils import cpp_extension as ext
     tmp = BIND + ".tmp%d" % os.getpid()
     inc = ext.include_paths("cuda") + [sysconfig.get_paths()["include"], os.path.join(ROOT, "include")]
     libs = ext.library_paths("cuda")
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-o", tmp, BIND_SOURCE]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", '-DLF_BIND_TAG="%s"' % tag.decode(), "-o", tmp, BIND_SOURCE]
     for d in inc:
         cmd += ["-isystem" if d != inc[-1] else "-I", d]
     for d in libs:
@@ -61,8 +71,13 @@ def build_bind(force: bool = False, verbose: bool = False) -> str:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
+    """The library and, where torch and g++ are there for it, the Python entry
+    of the paged-cache calls (build_bind raises where they are not)."""
     lib = build_lib(force, verbose)
-    build_bind(force, verbose)
+    try:
+        build_bind(force, verbose)
+    except (ImportError, OSError, subprocess.CalledProcessError) as e:
+        warnings.warn("_lf_bind.so, the Python entry of the paged-cache calls, is not built: %r" % e)
     return lib
 
 

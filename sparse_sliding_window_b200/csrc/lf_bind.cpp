@@ -263,7 +263,8 @@ PyMethodDef methods[] = {{"rope", (PyCFunction)(void *)rope, METH_FASTCALL, null
                          {"append", (PyCFunction)(void *)append, METH_FASTCALL, nullptr},
                          {"decode", (PyCFunction)(void *)decode, METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
-PyModuleDef module = {PyModuleDef_HEAD_INIT, "_lf_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+// the module's docstring names the torch it was built against
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_lf_bind", LF_BIND_TAG, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
 
