@@ -48,8 +48,8 @@ typedef struct lf_rope_params {
   int interleaved;          /* 0: pairs (p, p + rot_dim/2); 1: pairs (2p, 2p+1) */
   int n_axes;               /* positions per token, 1..4 */
   const int32_t *pair_axis; /* HOST [rot_dim/2], each in [0, n_axes); NULL = all 0 */
-  const double *freqs;      /* HOST [rot_dim/2], radians per position, finite; NULL: from base */
-  double base;              /* > 0; 0 => 10000 */
+  const double *freqs;      /* HOST [rot_dim/2], radians per position, of size at most 1e6; NULL: from base */
+  double base;              /* > 0, finite, no frequency above 1e6 (64 channels: base >= 6.5e-7); 0 => 10000 */
 } lf_rope_params;
 
 /* One tensor of a rotation: x and out are [B, heads, n, 64] with strides
@@ -58,7 +58,7 @@ typedef struct lf_rope_params {
 typedef struct lf_rope_tensor {
   const void *x;
   void *out;
-  int heads; /* >= 1 */
+  int heads; /* 1..128 */
   int64_t x_stride[3];
   int64_t out_stride[3];
 } lf_rope_tensor;

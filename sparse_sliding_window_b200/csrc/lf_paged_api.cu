@@ -47,6 +47,10 @@ static int lp_stride(int64_t &s, int64_t dim, int dtype, const char *name) {
 
 static const double LP_TWO_PI_HI = 6.283185307179586, LP_TWO_PI_LO = 2.4492935982947064e-16;
 
+// Radians per position: its product with an int32 position (below 2^31) is
+// within 2^48 turns, which double precision reduces to a turn without loss.
+static const double LP_MAX_FREQ = 1e6;
+
 static int lp_rope(const lf_rope_params *r, bool backward, LfRopeDev &d) {
   memset(&d, 0, sizeof(d));
   if (!r) return LF_OK;  // pairs = 0: nothing turns
@@ -67,7 +71,10 @@ static int lp_rope(const lf_rope_params *r, bool backward, LfRopeDev &d) {
     if (ax < 0 || ax >= r->n_axes) return lp_fail(LF_ERR_INVALID, "pair_axis[%d] = %d is no axis", p, ax);
     d.axis[p] = (uint8_t)ax;
     const double f = r->freqs ? r->freqs[p] : pow(base, -2.0 * p / rot);
-    if (!(fabs(f) <= 1e6)) return lp_fail(LF_ERR_INVALID, "freqs[%d] must be finite, at most 1e6", p);
+    if (!(fabs(f) <= LP_MAX_FREQ)) {
+      if (r->freqs) return lp_fail(LF_ERR_INVALID, "freqs[%d] must be finite, of size at most 1e6", p);
+      return lp_fail(LF_ERR_INVALID, "base %g is too small: pair %d turns by more than 1e6 radians a position", base, p);
+    }
     // f / 2 pi in twice double precision
     d.hi[p] = f / LP_TWO_PI_HI;
     d.lo[p] = (fma(-d.hi[p], LP_TWO_PI_HI, f) - d.hi[p] * LP_TWO_PI_LO) / LP_TWO_PI_HI;

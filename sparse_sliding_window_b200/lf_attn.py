@@ -365,8 +365,10 @@ def make_rope_params(rot_dim: int = 64, interleaved: bool = False, n_axes: int =
     r = lf_rope_params()
     r.rot_dim, r.interleaved, r.n_axes, r.base = rot_dim, int(interleaved), n_axes, float(base)
     if freqs is None and 2 <= rot_dim <= 64 and rot_dim % 2 == 0 and 0 < base < math.inf:
-        # what the library would compute at every call
-        freqs = [math.pow(base, -2.0 * p / rot_dim) for p in range(rot_dim // 2)]
+        # what the library would compute at every call (or refuse, naming the base)
+        logs = [-2.0 * p / rot_dim * math.log10(base) for p in range(rot_dim // 2)]
+        if max(logs) <= 6:
+            freqs = [math.pow(base, -2.0 * p / rot_dim) for p in range(rot_dim // 2)]
     for field, values, kind in (("pair_axis", pair_axis, ctypes.c_int32), ("freqs", freqs, ctypes.c_double)):
         if values is not None:
             if len(values) != (rot_dim or 64) // 2:
