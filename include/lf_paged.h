@@ -92,7 +92,7 @@ typedef struct lf_paged_params {
   int max_pages;           /* columns of the block table; max_pages*page_size <= 2^30 */
   int window;              /* r >= 0: keys (L-1) - k*d, k = 0..r; < 0: every row of the sequence */
   const int32_t *dilation; /* HOST [Hkv] of d >= 1 per key/value head, or NULL (all 1); all 1 when window < 0 */
-  float scale;             /* score scale; 0 => 1/sqrt(head_dim) */
+  float scale;             /* score scale, 0..2.3e38; 0 => 1/sqrt(head_dim) */
   int dtype;               /* LF_F32 / LF_BF16 / LF_F16 */
   int prefix_len;          /* rows of the prefix that the batch shares, 0..2^30 (0: none); row 0 of
                               a sequence stands at position prefix_len */

@@ -177,7 +177,8 @@ static int lp_prepare(const lf_paged_params *p, LfPagedLaunch &L) {
   if ((long long)p->max_pages * p->page_size > 1ll << 30)
     return lp_fail(LF_ERR_UNSUPPORTED, "max_pages * page_size must be at most 2^30");
   if (p->dtype < LF_F32 || p->dtype > LF_F16) return lp_fail(LF_ERR_INVALID, "bad dtype %d", p->dtype);
-  if (!(p->scale >= 0.f) || isinf(p->scale)) return lp_fail(LF_ERR_INVALID, "scale must be finite and >= 0");
+  if (!(p->scale >= 0.f) || isinf(p->scale * LF_LOG2E))
+    return lp_fail(LF_ERR_INVALID, "scale must be 0 .. 2.3e38 (got %g)", p->scale);
   if (p->prefix_len < 0 || p->prefix_len > 1 << 30)
     return lp_fail(LF_ERR_INVALID, "prefix_len must be 0..2^30 (got %d)", p->prefix_len);
   if (p->prefix_len > 0 && (long long)p->B * (p->H / p->Hkv) > 2000000)

@@ -41,3 +41,12 @@ def test_frequency_and_head_limits(lib):
     assert code == L.LF_ERR_INVALID and "freqs[31]" in text
     assert "x is NULL" in _rope(lib, L.make_rope_params(), 128)[1]
     assert "heads" in _rope(lib, L.make_rope_params(), 129)[1]
+
+
+PAGED = dict(B=2, H=4, Hkv=2, page_size=16, num_pages=9, max_pages=4, window=5, dtype=L.LF_BF16)
+
+
+def test_scale_that_overflows_in_base_2(lib):
+    """Scores are kept in base 2: scale * log2 e must be finite, too."""
+    for scale, fine in ((2.3e38, True), (2.4e38, False), (3.4e38, False)):
+        assert (L.lf_paged_workspace_size(L.make_paged_params(scale=scale, **PAGED)) > 0) == fine, scale
