@@ -115,10 +115,11 @@ size_t lf_paged_workspace_size(const lf_paged_params *p);
  *   q_out [T,H,64] contiguous; it may be q itself when q is contiguous
  * Left as they were: tokens of idle sequences and those >= cu_new[B] in
  * q_out, and every row of the pages that no token goes to.  A length outside
- * [0, max_pages*page_size], a token whose row would be < 0, a cu_new that
- * does not ascend and a page outside [0, num_pages) are recorded as
- * LF_ERR_DEVICE_INPUT; their tokens are skipped.  Two tokens that the table
- * sends to one row leave either of them there. */
+ * [0, max_pages*page_size], a token whose row would be < 0 and a page outside
+ * [0, num_pages) are recorded as LF_ERR_DEVICE_INPUT; their tokens are skipped.
+ * So is a cu_new that does not ascend from 0 to at most T: tokens that no
+ * sequence holds are skipped then, the others go to rows of one that does.
+ * Two tokens that the table sends to one row leave either of them there. */
 int lf_cache_append(const lf_paged_params *p, const lf_rope_params *rope, int T, const void *q,
                     const void *k, const void *v, const int64_t *strides, const int32_t *cu_new,
                     const int32_t *lengths, const int32_t *positions, const int32_t *block_table,

@@ -425,7 +425,8 @@ extern "C" int lf_attn_status(void *workspace, void *stream) {
   switch (code) {
     case LF_ERR_DEVICE_INPUT:
       if (det >= LF_DET_TOKENS)
-        return lf_fail(code, "sequence %d has new tokens without a cache row, or cu_new does not ascend", det - LF_DET_TOKENS);
+        return lf_fail(code, "sequence %d has new tokens without a cache row, or cu_new does not ascend from 0 to at most T there",
+                       det - LF_DET_TOKENS);
       if (det >= LF_DET_PREFIX) return lf_fail(code, "the prefix table holds a page outside the pool");
       if (det >= LF_DET_PAGE)
         return lf_fail(code, "sequence %d: the block table holds a page outside the pool", det - LF_DET_PAGE);

@@ -245,6 +245,16 @@ __global__ void __launch_bounds__(LF_ROPE_THREADS) lf_rope_kernel(const __grid_c
 #pragma unroll
       for (int w = 0; w < NV; w++) v[u][w] = ahead[u][w];
   }
+
+  // cu_new ascends from 0 to at most the tokens there are: all of it is looked
+  // at, as the search above reads only a few entries (and finds a sequence in
+  // offsets that are none, too).
+  if (APPEND && A.cu && blockIdx.y == 0)
+    for (int b = blockIdx.x * LF_ROPE_THREADS + threadIdx.x; b < A.B; b += gridDim.x * LF_ROPE_THREADS) {
+      const int c0 = A.cu[b], c1 = A.cu[b + 1];
+      if (c1 < c0 || (b == 0 && c0 != 0) || (b == A.B - 1 && c1 > A.tokens))
+        lf_set_status(A.status, LF_ERR_DEVICE_INPUT, LF_DET_TOKENS + b);
+    }
 }
 
 template <typename T, int KIND, bool APPEND>
