@@ -424,14 +424,15 @@ extern "C" int lf_attn_status(void *workspace, void *stream) {
   const int code = w[LF_ST_CODE], det = w[LF_ST_DETAIL];
   switch (code) {
     case LF_ERR_DEVICE_INPUT:
-      if (det >= LF_DET_TOKENS)
-        return lf_fail(code, "sequence %d has new tokens without a cache row, or cu_new does not ascend from 0 to at most T there",
-                       det - LF_DET_TOKENS);
-      if (det >= LF_DET_PREFIX) return lf_fail(code, "the prefix table holds a page outside the pool");
-      if (det >= LF_DET_PAGE)
-        return lf_fail(code, "sequence %d: the block table holds a page outside the pool", det - LF_DET_PAGE);
-      if (det >= LF_DET_LENGTH)
+      if (det < 0) {
+        if (det >= LF_DET_TOKENS)
+          return lf_fail(code, "sequence %d has new tokens without a cache row, or cu_new does not ascend from 0 to at most T there",
+                         det - LF_DET_TOKENS);
+        if (det >= LF_DET_PREFIX) return lf_fail(code, "the prefix table holds a page outside the pool");
+        if (det >= LF_DET_PAGE)
+          return lf_fail(code, "sequence %d: the block table holds a page outside the pool", det - LF_DET_PAGE);
         return lf_fail(code, "sequence %d has a length outside its block table", det - LF_DET_LENGTH);
+      }
       if (det >= 2000000)
         return lf_fail(code, "sequence %d has more global tokens than max_global", det - 2000000);
       return lf_fail(code, "sequence %d has a mask value outside {0,1,2}", det - 1000000);

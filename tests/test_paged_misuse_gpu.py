@@ -59,3 +59,18 @@ def test_append_records_offsets_of_many_idle_sequences():
     with pytest.raises(L.LfError) as e:
         L.lf_attn_status(ws)
     assert "sequence 2899" in str(e.value)
+
+
+def test_mask_errors_of_large_batches_keep_their_text():
+    """The status details of the paged calls do not overlap those of the mask pass, whatever the batch."""
+    import torch
+    B = 2000001
+    p = L.make_params(B, 1, 2, 0, None, False, 0.0, L.LF_BF16, 1)
+    ws = L.workspace(p)
+    mask = torch.ones(B, 2, dtype=torch.int32, device="cuda")
+    mask[B - 1] = 2                                     # two global tokens, and one is allowed
+    counts = torch.empty(B, 1, dtype=torch.int64, device="cuda")
+    L.lf_attn_count_pairs(p, mask, counts, ws)
+    with pytest.raises(L.LfError) as e:
+        L.lf_attn_status(ws)
+    assert "sequence %d has more global tokens" % (B - 1) in str(e.value)
