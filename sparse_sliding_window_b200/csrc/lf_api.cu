@@ -15,7 +15,7 @@
 
 #include "lf_attn.h"
 #include "lf_common.cuh"
-#include "lf_paged.cuh"
+#include "lf_status.cuh"
 #include "lf_tc.cuh"
 
 static thread_local char g_err[512];
@@ -431,7 +431,9 @@ extern "C" int lf_attn_status(void *workspace, void *stream) {
         if (det >= LF_DET_PREFIX) return lf_fail(code, "the prefix table holds a page outside the pool");
         if (det >= LF_DET_PAGE)
           return lf_fail(code, "sequence %d: the block table holds a page outside the pool", det - LF_DET_PAGE);
-        return lf_fail(code, "sequence %d has a length outside its block table", det - LF_DET_LENGTH);
+        if (det >= LF_DET_LENGTH)
+          return lf_fail(code, "sequence %d has a length outside its block table", det - LF_DET_LENGTH);
+        return lf_fail(code, "sequence %d has more selected rows than max_rows", LF_DET_ROWS - det);
       }
       if (det >= 2000000)
         return lf_fail(code, "sequence %d has more global tokens than max_global", det - 2000000);

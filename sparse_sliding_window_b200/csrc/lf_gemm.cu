@@ -43,6 +43,7 @@
 #include "lf_common.cuh"
 #include "lf_proj.h"
 #include "lf_ptx.cuh"
+#include "lf_status.cuh"
 #include "lf_tc.cuh"
 
 #define LG_BM 128
@@ -400,7 +401,7 @@ __global__ void __launch_bounds__(1024)
   const int cnt = min(s_total, max_rows);
   if (tid == 0) {
     count[b] = cnt;
-    if (s_total > max_rows) lf_set_status(status, LF_ERR_DEVICE_INPUT, 4000000 + b);
+    if (s_total > max_rows) lf_set_status(status, LF_ERR_DEVICE_INPUT, LF_DET_ROWS - b);
   }
   __syncthreads();  // rows[] written
   // copy the selected rows, 16 bytes per thread per step

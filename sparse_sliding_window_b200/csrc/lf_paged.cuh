@@ -5,17 +5,11 @@
 #include "lf_common.cuh"
 #include "lf_paged.h"
 #include "lf_pages.cuh"
+#include "lf_status.cuh"
 
 #define LF_ROPE_MAX_PAIRS 32
 #define LF_ROPE_MAX_AXES 4
 #define LF_ROPE_MAX_JOBS 8
-
-// details of LF_ERR_DEVICE_INPUT in the status word (+ the sequence, below
-// 999999): negative, as those of the mask pass are 1000000 and more without end
-#define LF_DET_LENGTH (-4000000)  // length outside [0, capacity]
-#define LF_DET_PAGE (-3000000)    // block table entry outside [0, num_pages)
-#define LF_DET_PREFIX (-2000000)  // prefix table entry outside [0, num_pages)
-#define LF_DET_TOKENS (-1000000)  // new tokens without a row, or cu_new not ascending
 
 // Turns (angle / 2 pi) per position of each pair, as hi + lo.
 struct LfRopeDev {

@@ -74,3 +74,18 @@ def test_mask_errors_of_large_batches_keep_their_text():
     with pytest.raises(L.LfError) as e:
         L.lf_attn_status(ws)
     assert "sequence %d has more global tokens" % (B - 1) in str(e.value)
+
+
+def test_too_many_selected_rows_are_reported_as_that():
+    import torch
+    B, n, H = 2, 8, 4
+    p = L.make_proj_params(B, n, H)
+    ws = L.proj_workspace(p, 2)
+    dt = torch.bfloat16
+    x, w, b = (torch.zeros(*s, dtype=dt, device="cuda") for s in ((B, n, H * 64), (H * 64, H * 64), (H * 64,)))
+    mask = torch.ones(B, n, dtype=torch.int32, device="cuda")
+    mask[1, :3] = 2
+    L.lf_proj_in(p, x, w, b, [torch.zeros(B, H, n, 64, dtype=dt, device="cuda")], ws, rows_mask=mask, rows_code=2, max_rows=2)
+    with pytest.raises(L.LfError) as e:
+        L.lf_attn_status(ws)
+    assert e.value.code == L.LF_ERR_DEVICE_INPUT and "sequence 1 has more selected rows" in str(e.value)
