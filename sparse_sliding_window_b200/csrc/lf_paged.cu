@@ -64,11 +64,11 @@ __device__ __forceinline__ void lf_pd_begin(bool prefix) {
 // in flight.  Every sub-warp of 64/N lanes keeps its own running maximum, sum
 // and output for the rows it reads; they are merged once, at the end, through
 // registers, shared memory and distributed shared memory.
-template <typename T, int GT>
+template <int GT>
 __global__ void __launch_bounds__(LF_PD_WARPS * 32)
-    lf_paged_decode_kernel(const __grid_constant__ LfPagedDev P, const T *q, const T *kp, const T *vp, T *o,
-                           float *lse, int ngroups, int cl) {
-  constexpr int N = LfVec<T>::N;
+    lf_paged_decode_kernel(const __grid_constant__ LfPagedDev P, const float *q, const float *kp, const float *vp,
+                           float *o, float *lse, int ngroups, int cl) {
+  constexpr int N = LfVec<float>::N;
   constexpr int LPR = LF_HD / N;        // lanes per row
   constexpr int SUB = 32 / LPR;         // rows per warp load
   constexpr int BATCH = SUB * LF_PD_LOADS;
@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(LF_PD_WARPS * 32)
 #pragma unroll
     for (int j = 0; j < N; j++) qf[g][j] = acc[g][j] = 0.f;
     if (g < gn && nk > 0) {
-      LfVec<T>::ld(q + b * P.qs[0] + (hk * P.G + g0 + g) * P.qs[1] + lr * N, qf[g]);
+      LfVec<float>::ld(q + b * P.qs[0] + (hk * P.G + g0 + g) * P.qs[1] + lr * N, qf[g]);
 #pragma unroll
       for (int j = 0; j < N; j++) qf[g][j] *= P.scale_log2;
     }
@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(LF_PD_WARPS * 32)
 #pragma unroll
     for (int i = 0; i < LF_PD_LOADS; i++) {
       float x[N];
-      LfVec<T>::ld(reinterpret_cast<const T *>(&kr[i]), x);
+      LfVec<float>::ld(reinterpret_cast<const float *>(&kr[i]), x);
 #pragma unroll
       for (int g = 0; g < GT; g++) {
         float a = 0.f;
@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(LF_PD_WARPS * 32)
 #pragma unroll
     for (int i = 0; i < LF_PD_LOADS; i++) {
       float x[N];
-      LfVec<T>::ld(reinterpret_cast<const T *>(&vr[i]), x);
+      LfVec<float>::ld(reinterpret_cast<const float *>(&vr[i]), x);
 #pragma unroll
       for (int g = 0; g < GT; g++)
 #pragma unroll
@@ -332,7 +332,7 @@ static cudaError_t lf_launch_pd_f32(const LfPagedLaunch &L, const void *q, const
   const int ngroups = (P.G + GT - 1) / GT;
   const int64_t units = (int64_t)P.B * P.Hkv * ngroups;
   const int cl = lf_pd_cluster(P, units, BATCH * LF_PD_WARPS, 8);
-  return lf_pd_launch((const void *)lf_paged_decode_kernel<float, GT>, L, units, cl,
+  return lf_pd_launch((const void *)lf_paged_decode_kernel<GT>, L, units, cl,
                       cl > 1 ? cl * GT * (LF_HD + 2) * 4 : 0, q, kp, vp, o, lse, ngroups);
 }
 
