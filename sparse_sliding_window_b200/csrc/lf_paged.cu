@@ -282,11 +282,15 @@ static int64_t lf_most_keys(const LfPagedDev &P) {
 // Few units (sequence, key/value head): the decode kernel reads the prefix for
 // every sequence itself, which saves a kernel and the merging of its parts.
 // With up to 37 units (8 CTAs each, two per SM) the repeated reads come from L2
-// and keep up to about here.  Measured, prefix kernel / direct, in us: f32 1 x 8
-// heads 1000 rows 8.4 / 5.7, 4000 rows 21.9 / 10.5; f32 36 x 1 heads 10.3 / 6.4
-// and 13.4 / 12.5; bf16 2 x 32/4 heads 2000 rows 12.3 / 7.5, 8000 rows 33.7 /
-// 11.1; bf16 36 x 1 heads 9.1 / 7.3 and 12.8 / 13.2; bf16 4 x 8 heads 6.3 / 7.4
-// and 14.1 / 13.2.
+// and keep up to about here.  Measured, prefix kernel / direct, in us, on 300,
+// 1000, 4096 and 8192 rows with a window of 64: bf16 1 x 8 heads 5.1 / 4.2, 5.1 /
+// 5.0, 8.6 / 7.6, 13.4 / 10.7; 36 x 1 heads 7.1 / 4.9, 8.0 / 6.6, 12.5 / 11.3,
+// 12.9 / 16.6; 2 x 32/4 heads 9.8 / 5.9, 9.2 / 6.9, 19.0 / 9.4, 32.5 / 12.6;
+// f32 1 x 8 heads 7.9 / 4.0, 8.0 / 5.8, 20.0 / 11.6, 33.8 / 29.2; 36 x 1 heads
+// 9.7 / 4.6, 9.8 / 6.6, 11.4 / 14.5, 15.5 / 24.8.  The rule goes by the units and
+// the prefix alone, and is off by up to a quarter where a few sequences of one
+// query head per key/value head leave the prefix kernel many heads: bf16 4 x 8
+// heads 5.2 / 4.6, 5.1 / 6.6, 9.3 / 11.3, 14.0 / 16.6.
 bool lf_prefix_direct(const LfPagedDev &P, int dtype) {
   const int64_t units = (int64_t)P.B * P.Hkv * ((P.G + 15) / 16);
   return units * 8 <= 2 * 148 && P.prefix_len <= (dtype == LF_F32 ? 4096 : 8192);
@@ -832,8 +836,9 @@ static int lf_pdr_smem(const LfPagedDev &P) {
   return LF_PM_RING + 4 * wrows * LF_HD * 4 + (P.nch > 0 ? lf_pd_fold_bytes(wrows, P.nch) : 0) + 2 * P.B * 4;
 }
 
-// CTAs of the run kernel: as many as fit a full B200 at once (two per SM, one
-// where the rings and the lengths leave no room for the second).
+// CTAs of the run kernel: as many as fit a full B200 at once: three per SM (two
+// for groups of more than 16 query heads, whose states take 255 registers), fewer
+// where the rings and the lengths leave no room for them.
 void lf_paged_plan(LfPagedDev &P, int dtype) {
   P.run_ctas = 0;
   P.same_dil = 1;
@@ -846,7 +851,19 @@ void lf_paged_plan(LfPagedDev &P, int dtype) {
   // no list.  Measured, clusters / runs, bf16, in us: 16 units of 8 heads with a
   // window of 257 keys 4.3 / 6.5, 64 units 5.5 / 6.6, 144 units 9.7 / 8.1; every
   // row up to 4000: 32 units 9.0 / 11.0, 64 units 16.4 / 15.5, 128 units 29.0 /
-  // 25.1; up to 16000: 16 units 19.4 / 25.6, 64 units 36.6 / 34.6.
+  // 25.1; up to 16000: 16 units 19.4 / 25.6, 64 units 36.6 / 34.6.  One sequence
+  // of 1, 4, 16 and 32 heads: 8000 rows 9.5 / 12.3, 9.8 / 13.2, 12.3 / 14.3, 16.6 /
+  // 20.0; 24000 rows 21.6 / 22.8, 22.2 / 24.1, 28.1 / 26.3, 38.1 / 39.8; 128000
+  // rows 104 / 57, 105 / 39, 128 / 91, 183 / 169, but with 8 query heads to each
+  // of 1 and 4 key/value heads 25.5 / 85.0 and 24.4 / 76.7 for 24000 rows, 106 /
+  // 198 and 107 / 79 for 128000, as one CTA adds all parts of a unit.  Rows are
+  // known here only as the table's capacity, which most sequences do not fill, so
+  // the rule goes by the units.
+  // Larger batches than the list's limits, clusters / runs: 1100 x 4 heads, 300
+  // rows 60.5 / 59.7, the same behind 2000 rows of prefix 35.5 / 48.5, 2000 x 2
+  // heads 72.7 / 96.6 (every CTA reads all lengths), but 1100 x 12 heads 114 / 87;
+  // 40000 units 316 / 215, for which the counters would take four times the
+  // workspace.
   const int few = P.nch == 0 && keys <= 512 ? 4 * 148 : 2 * 148;
   if (units * 8 <= few || units > LF_PDR_MAX_UNITS || tiles >= 1ll << 31) return;
   const int per = 228 * 1024 / (lf_pdr_smem(P) + 1024 + 640);  // 1 KB of the system's, 640 static

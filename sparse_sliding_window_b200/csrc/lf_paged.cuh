@@ -67,10 +67,12 @@ struct LfPagedDev {
 #define LF_PART_MAX 64          // parts per row at most
 #define LF_PDR_MAX_UNITS 32768  // units with a counter
 #define LF_PDR_MAX_B 1024  // sequences whose lengths the decode kernel keeps in shared memory
-// Units up to so many tiles are not cut.  Measured, whole / cut, bf16, in us,
-// with windows of 257 keys: 12 x 12 heads 8.2 / 11.2, 32 x 16/4 heads 8.6 / 13.6,
-// 64 x 12 heads (fp16) 15.5 / 17.5.
-#define LF_PDR_WHOLE 6
+// Units up to so many tiles are not cut.  Measured, whole / cut, in us: three
+// tiles (window 256), 64 x 12 heads (f16) 15.8 / 18.1, 12 x 12 (bf16) 8.2 / 8.1,
+// 32 x 16/4 8.6 / 9.7; four tiles 19.8 / 21.9, 9.8 / 9.5, 10.1 / 10.5; five tiles
+// (window 512) 23.7 / 25.7, 11.3 / 11.5, 11.6 / 13.5; six tiles 27.5 / 29.7, but
+// 12.8 / 10.3 and 13.1 / 11.6.
+#define LF_PDR_WHOLE 5
 
 cudaError_t lf_launch_rope(const LfRopeArgs &a, int dtype, bool append, cudaStream_t stream);
 

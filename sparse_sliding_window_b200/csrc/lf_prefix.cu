@@ -181,9 +181,13 @@ __global__ void __launch_bounds__(128, 2) lf_prefix_mma_kernel(const __grid_cons
 // The tensor-core kernel's tile has 128 rows: it takes over where the rows no
 // longer fit one block of the warp-level kernel (which would read the prefix
 // once per 32 rows).  Measured, warp-level / tensor-core, bf16, whole calls with a
-// window of 64, in us: 40 x 12 heads 500 rows 13.4 / 14.8, 4096 rows 21.8 / 17.6;
-// 64 x 12 heads 16.1 / 15.3 and 26.1 / 18.4; 128 x 12 heads 23.5 / 23.8 and 38.6 /
-// 28.1.
+// window of 64, in us, on 500, 1000, 2000 and 4096 rows: 40 x 12 heads 13.7 /
+// 14.6, 13.8 / 14.8, 18.0 / 14.0, 21.3 / 16.2; 64 x 12 heads 15.5 / 16.1, 17.5 /
+// 16.5, 22.6 / 17.8, 26.5 / 20.3; 128 x 12 heads 24.4 / 24.9, 28.5 / 25.7, 31.3 /
+// 28.1, 38.3 / 30.1; 64 x 16/4 heads 12.3 / 12.1, 14.3 / 13.4, 19.6 / 13.9, 22.7 /
+// 15.4.  By the rows alone it is up to a fifth off on prefixes of 1000 and 2000
+// rows for few of them: 20 x 16/4 heads 8.6 / 8.5, 8.5 / 9.6, 10.9 / 13.0, 16.1 /
+// 13.5.
 static bool lf_prefix_is_tc(const LfPagedDev &d, int dtype) { return dtype != LF_F32 && (int64_t)d.B * d.G > 32; }
 
 static int lf_prefix_rows(const LfPagedDev &d, int dtype) {

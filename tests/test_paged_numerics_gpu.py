@@ -309,3 +309,17 @@ def test_captured_steps_follow_what_kernels_write(B, H, Hkv, prefix, dtype):
         torch.cuda.synchronize()
         assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
     assert all(torch.equal(x.view(torch.int16), y.view(torch.int16)) for x, y in ((c.k, kp), (c.v, vp)))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("window", [384, 511, 512, 639, 640, 768])
+@pytest.mark.parametrize("B,H,Hkv", [(20, 8, 4), (26, 40, 2)])
+def test_units_of_a_few_tiles(B, H, Hkv, window, dtype):
+    """Windows around the number of tiles up to which a unit stays in one block."""
+    c = Cache(909, dtype, B, Hkv, 32, [(700 + 61 * b) % 900 for b in range(B)])
+    q = _normal_like(c, _one_channel_query(B, H, dtype))
+    o, lse = _decode(c, q, H, window)
+    half = R.half_step(dtype)
+    ref, rl, to, tl = _reference(c, q, H, window, None, 0.125, (2 * half) ** 2)
+    R.check("o", R.f64(o), ref, to + 2.0 ** -25 + half * (np.abs(ref) + to))
+    R.check("lse", R.f64(lse), rl, tl)
