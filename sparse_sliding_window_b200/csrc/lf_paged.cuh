@@ -164,12 +164,13 @@ __device__ __forceinline__ void lf_p_split(float p0, float p1, uint32_t &high, u
     r0 = p0 - h0;
     r1 = p1 - h1;
   }
-  // `low` is at least the type's smallest positive number (2^-31 of the largest
-  // p, or less): 0 times an infinite value would be NaN.
+  // Unless p is 0 in the type, `low` is at least the type's smallest positive
+  // number (2^-31 of the largest p, or less): 0 times an infinite value would be
+  // NaN.  (bf16: the smallest normal one, as a product may flush others to 0.)
   if (kF16)
-    asm("{\n\t.reg .b32 r;\n\tcvt.rn.f16x2.f32 r, %1, %2;\n\tmax.f16x2 %0, r, %3;\n\t}"
-        : "=r"(low) : "f"(r1), "f"(r0), "r"(0x00010001u));
-  else  // the smallest normal number: the product may flush smaller ones to 0
-    asm("{\n\t.reg .b32 r;\n\tcvt.rn.bf16x2.f32 r, %1, %2;\n\tmax.bf16x2 %0, r, %3;\n\t}"
-        : "=r"(low) : "f"(r1), "f"(r0), "r"(0x00800080u));
+    asm("{\n\t.reg .b32 r, t;\n\tcvt.rn.f16x2.f32 r, %1, %2;\n\tmin.f16x2 t, %4, %3;\n\tmax.f16x2 %0, r, t;\n\t}"
+        : "=r"(low) : "f"(r1), "f"(r0), "r"(0x00010001u), "r"(high));
+  else
+    asm("{\n\t.reg .b32 r, t;\n\tcvt.rn.bf16x2.f32 r, %1, %2;\n\tmin.bf16x2 t, %4, %3;\n\tmax.bf16x2 %0, r, t;\n\t}"
+        : "=r"(low) : "f"(r1), "f"(r0), "r"(0x00800080u), "r"(high));
 }

@@ -323,3 +323,24 @@ def test_units_of_a_few_tiles(B, H, Hkv, window, dtype):
     ref, rl, to, tl = _reference(c, q, H, window, None, 0.125, (2 * half) ** 2)
     R.check("o", R.f64(o), ref, to + 2.0 ** -25 + half * (np.abs(ref) + to))
     R.check("lse", R.f64(lse), rl, tl)
+
+
+@pytest.mark.parametrize("dtype", R.DTYPES)
+@pytest.mark.parametrize("path", PATHS)
+def test_keys_of_probability_zero_weigh_nothing(path, dtype):
+    """Every other key has score -inf and the type's largest value: the output
+    is that of the same rows with values of 0 there, to the bit."""
+    import torch
+    B, H, Hkv, prefix, n = PATHS[path]
+    c = Cache(910, dtype, B, Hkv, 16, [n] * B, prefix)
+    q = _normal_like(c, _one_channel_query(B, H, dtype))
+    q[..., 0] = 1
+    dead = [(table[j // 16], j % 16) for table, m in [(c.table[b], n) for b in range(B)] + [(c.prefix_table, prefix)]
+            for j in range(1, m, 2)]
+    page, slot = (torch.tensor(x, device="cuda") for x in zip(*[(int(p), s) for p, s in dead]))
+    c.k[page, :, slot, 0] = -math.inf
+    c.v[page, :, slot] = 0
+    want, wl = _decode(c, q, H)
+    c.v[page, :, slot] = torch.finfo(c.v.dtype).max
+    o, lse = _decode(c, q, H)
+    assert torch.equal(o, want) and torch.equal(lse, wl) and torch.isfinite(o).all()
