@@ -139,9 +139,11 @@ int lf_cache_append(const lf_paged_params *p, const lf_rope_params *rope, int T,
  * nothing, or scores of -inf alone, gets o = 0 and lse = -inf, and so does one
  * whose length is outside [0, max_pages*page_size].  Such a length and a page
  * outside [0, num_pages) (its rows are left out) are recorded as
- * LF_ERR_DEVICE_INPUT.  An infinite value of an attended row makes its channel
- * infinite, or NaN where the row's probability is 0 in the tensors' type.
- * Results do not depend on the order in which blocks run. */
+ * LF_ERR_DEVICE_INPUT.  Scores, sums and the softmax are float32, and a 16-bit
+ * output is rounded once, whichever kernel runs.  An infinite value of an
+ * attended row makes its channel infinite, or NaN where another one's sign
+ * differs or the row's probability is 0 in the tensors' type.  Results do not
+ * depend on the order in which blocks run. */
 int lf_paged_decode(const lf_paged_params *p, const void *q, const int64_t *q_stride,
                     const void *k_pages, const void *v_pages, const int32_t *block_table,
                     const int32_t *lengths, const int32_t *prefix_table, void *o, float *lse,

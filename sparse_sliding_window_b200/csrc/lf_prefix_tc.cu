@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(LF_PT_THREADS, 1) lf_prefix_tc_kernel(const __
         // P enters the product with V as two 16-bit numbers: the first through
         // TMEM, the second, for which TMEM has no room, through shared memory.
         // (One number alone: 128 x 16/4 heads on 16384 rows 38.4 us instead of
-        // 43.0, 64 x 12 heads on 4096 rows 25.8 instead of 27.3.)
+        // 43.2, 64 x 12 heads on 4096 rows 25.8 instead of 27.8.)
         uint8_t *low = lf_smem_raw + LF_PT_L(g) + row * 128;
         // The scaling and the subtraction of the reference are one operation where
         // the reference's own rounding is far below 1 (at most 2^-4).  Beyond, the

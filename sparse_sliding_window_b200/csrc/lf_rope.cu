@@ -2,8 +2,9 @@
 // append of new tokens to the paged cache with that rotation on the way.
 //
 // Both move every element once and compute a few operations for it, so they
-// are bound by memory: 269 MB in 46.5 us (5.8 TB/s, 0.88 of a plain copy's
-// rate) for bf16 queries and keys of 2 x 16 heads x 16384 tokens.  A thread keeps one 16-byte slice (two for pairs
+// are bound by memory: 269 MB in 48.0 us per call (5.6 TB/s, 0.85 of a plain
+// copy's rate; 46.5 us in graph replays) for bf16 queries and keys of 2 x 16
+// heads x 16384 tokens.  A thread keeps one 16-byte slice (two for pairs
 // (p, p + rot/2), so that both halves of its pairs are in its registers) of
 // one token and works through heads: the cosines and sines, the same for
 // every head of a token, are computed once per thread.
