@@ -57,6 +57,21 @@ cudaError_t lf_kernel_smem(const void *fn, int smem_bytes) {
   return e;
 }
 
+typedef CUresult (*LfCtxGetCurrent)(CUcontext *);
+cudaError_t lf_need_context() {
+  static const LfCtxGetCurrent get = [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const cudaError_t e = cudaGetDriverEntryPoint("cuCtxGetCurrent", &p, cudaEnableDefault, &q);
+    return (LfCtxGetCurrent)(e == cudaSuccess && q == cudaDriverEntryPointSuccess ? p : nullptr);
+  }();
+  CUcontext ctx = nullptr;
+  if (get && get(&ctx) == CUDA_SUCCESS && ctx) return cudaSuccess;
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  return e == cudaSuccess ? cudaSetDevice(dev) : e;
+}
+
 int lf_sm_count() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 148;
@@ -246,6 +261,7 @@ extern "C" int lf_attn_fwd(const lf_attn_params *p, const void *q_s, const void 
   if (tc) {
     // the tensor-core path launches the mask pass itself; a shape outside its
     // parameter block is refused (LF_ERR_UNSUPPORTED), never run elsewhere
+    if ((st = lf_cuda(lf_need_context(), "context"))) return st;
     LfTcArgs a{q_s, k_s, v_s, q_g, k_g, v_g, o, lse, g_ev_start, g_ev_stop};
     if ((st = lf_tc_fwd(L, a, g_err, sizeof(g_err)))) return st;
   } else {
@@ -408,6 +424,7 @@ extern "C" int lf_attn_cross_fwd(const lf_cross_params *p, const void *q, const 
   L.dev.gidx = L.dev.grank = nullptr;
   L.dev.wait_us = g_test_wait_us;
   L.dev.skip_tile = g_test_skip_tile;
+  if ((st = lf_cuda(lf_need_context(), "context"))) return st;
   return lf_tc_cross_fwd(L, q, k, v, o, lse, g_ev_start, g_ev_stop, g_err, sizeof(g_err));
 }
 

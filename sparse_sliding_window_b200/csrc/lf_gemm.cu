@@ -550,6 +550,7 @@ static int lg_bind(const lf_proj_params *p, int max_rows, void *workspace, size_
   w = lg_ws(p, max_rows);
   if (ws_bytes < w.total) return lf_record_error(LF_ERR_INVALID, "workspace too small");
   (void)stream;
+  if ((st = lg_cuda(lf_need_context(), "context"))) return st;
   return LF_OK;  // the status word stays set until lf_attn_status reads and clears it
 }
 

@@ -525,6 +525,8 @@ void lf_prefix_tc_plan(LfPagedDev &d) {
 
 template <typename T, int kF16>
 static cudaError_t lf_launch_prefix_tc_t(const LfPagedLaunch &L, const void *q, const void *kp, const void *vp) {
+  cudaError_t e = lf_need_context();
+  if (e != cudaSuccess) return e;
   LfPtParams A;
   A.dev = L.dev;
   A.q = q;
@@ -535,7 +537,7 @@ static cudaError_t lf_launch_prefix_tc_t(const LfPagedLaunch &L, const void *q, 
       !lf_make_map(&A.v, kF16, vp, rows, 1, 1, 128, rows * 128, rows * 128, A.box_rows))
     return cudaErrorInvalidValue;
   const void *fn = (const void *)lf_prefix_tc_kernel<T, kF16>;
-  const cudaError_t e = lf_kernel_smem(fn, LF_PT_SMEM);
+  e = lf_kernel_smem(fn, LF_PT_SMEM);
   if (e != cudaSuccess) return e;
   const int64_t rblocks = ((int64_t)P.B * P.G + LF_PT_ROWS - 1) / LF_PT_ROWS;
   if (rblocks > 65535) return cudaErrorInvalidConfiguration;

@@ -21,6 +21,12 @@ struct LfTcSeg {
   int h0, h1, d, rho, cnt, nqb, start, map;
 };
 
+// Makes the current device's context current to the calling host thread if none
+// is: a thread that has made no runtime call of its own has none, and encoding
+// a tensor map (a driver call) needs one.  Calls that encode maps before they
+// launch anything begin with it.
+cudaError_t lf_need_context();
+
 // 4-D tiled TMA map over rows of 64 elements: dims {64, rows, H, B}, byte
 // strides {row, head, batch}, box {64, box_rows, 1, 1}, 128-byte swizzle.
 bool lf_make_map(CUtensorMap *m, int f16, const void *base, uint64_t rows, uint64_t H, uint64_t B,
