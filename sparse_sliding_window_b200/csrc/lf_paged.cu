@@ -287,10 +287,11 @@ static int64_t lf_most_keys(const LfPagedDev &P) {
 // 5.0, 8.6 / 7.6, 13.4 / 10.7; 36 x 1 heads 7.1 / 4.9, 8.0 / 6.6, 12.5 / 11.3,
 // 12.9 / 16.6; 2 x 32/4 heads 9.8 / 5.9, 9.2 / 6.9, 19.0 / 9.4, 32.5 / 12.6;
 // f32 1 x 8 heads 7.9 / 4.0, 8.0 / 5.8, 20.0 / 11.6, 33.8 / 29.2; 36 x 1 heads
-// 9.7 / 4.6, 9.8 / 6.6, 11.4 / 14.5, 15.5 / 24.8.  The rule goes by the units and
-// the prefix alone, and is off by up to a quarter where a few sequences of one
-// query head per key/value head leave the prefix kernel many heads: bf16 4 x 8
-// heads 5.2 / 4.6, 5.1 / 6.6, 9.3 / 11.3, 14.0 / 16.6.
+// 9.7 / 4.6, 9.8 / 6.6, 11.4 / 14.5, 15.5 / 24.8; 2 x 32/4 heads (four at a time,
+// though counted by sixteen) 10.4 / 5.8, 10.5 / 8.9, 18.7 / 20.5, 25.4 / 36.0.
+// The rule goes by the units and the prefix alone, and is off by up to a quarter
+// where a few sequences of one query head per key/value head leave the prefix
+// kernel many heads: bf16 4 x 8 heads 5.2 / 4.6, 5.1 / 6.6, 9.3 / 11.3, 14.0 / 16.6.
 bool lf_prefix_direct(const LfPagedDev &P, int dtype) {
   const int64_t units = (int64_t)P.B * P.Hkv * ((P.G + 15) / 16);
   return units * 8 <= 2 * 148 && P.prefix_len <= (dtype == LF_F32 ? 4096 : 8192);
